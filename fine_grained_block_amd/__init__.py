@@ -10,6 +10,7 @@ fallback: if the library is missing, or a call returns a nonzero status, an exce
     w_q, s_w = quantize_weight(w, "ue8m0")
     y = gemm(q, s_a, w_q, s_w)           # bf16 [M, N]
     y = grouped_gemm(q, s_a, w_q, s_w, offsets)
+    y = gemm_epilogue(q, s_a, w_q, s_w, bias=b, activation="silu", residual=r)
 """
 from ._lib import (  # noqa: F401
     FGBError,
@@ -37,6 +38,7 @@ from .ops import (  # noqa: F401
     quantize_static,
     scaled_gemm,
     gemm,
+    gemm_epilogue,
     gemm_noalloc,
     gemm_fused_quant,
     gemm_fused_quant_workspace_bytes,

@@ -12,6 +12,7 @@ ACT_SCALE_GROUP128, ACT_SCALE_TOKEN, ACT_SCALE_TENSOR = 0, 1, 2
 W_SCALE_BLOCK128, W_SCALE_CHANNEL = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 FP8_E4M3, FP8_E5M2, UE8M0, FP8_E4M3_INT = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 
 _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -25,6 +26,10 @@ _SIGS = {
                                            _c_i64, _c_i64, _c_i64, _c_i64, _vp, ctypes.c_size_t, _vp]),
     "fgb_w8a8_block_gemm_noalloc": (ctypes.c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _vp, ctypes.c_int, _vp,
                                                    ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _vp]),
+    "fgb_w8a8_block_gemm_epilogue": (ctypes.c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _vp, ctypes.c_int, _vp,
+                                                    ctypes.c_int, ctypes.c_int, _vp, ctypes.c_int, _c_i64, _vp,
+                                                    ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _vp,
+                                                    ctypes.c_size_t, _vp]),
     "fgb_gemm_fused_quant_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
     "fgb_w8a8_block_gemm_fused_quant": (ctypes.c_int, [_vp, _c_i64, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int,
                                                        _c_i64, _c_i64, _c_i64, _c_i64, _vp, ctypes.c_size_t, _vp]),

@@ -1,0 +1,106 @@
+// epilogue.hpp — what the epilogue GEMM does to a finished sum: y = act(sum + bias) + residual, in
+// float32, rounded once when y is stored.
+//
+//   relu       max(v, 0)
+//   gelu       v * Phi(v) = v/2 * erfc(-v / sqrt 2): the complementary function keeps the relative
+//              accuracy of the negative tail, where 1 + erf cancels
+//   gelu_tanh  v/2 * (1 + tanh u) = v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
+//   silu       v * sigmoid(v)
+// sigmoid(z) = 1 / (1 + exp(-z)): for z -> -inf the exponential is +inf and the quotient 0, so no
+// form overflows into a NaN.
+#pragma once
+#include "gemm_common.hpp"
+#include "internal.h"
+
+namespace fgb {
+
+__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
+
+__device__ __forceinline__ float gelu_tanh(float v) {
+  const float u = 0.79788456080286536f * __builtin_fmaf(0.044715f * v * v, v, v);
+  return v * sigmoidf(2.0f * u);
+}
+
+// act is uniform over the launch.
+template <int W>
+__device__ __forceinline__ void activate(int act, float (&v)[W]) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] *= sigmoidf(v[i]);
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = gelu_tanh(v[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = gelu_erf(v[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = fmaxf(v[i], 0.0f);
+  }
+}
+
+// W (4 or 8) consecutive values of a bf16 (dtype 0) or float32 (dtype 1) array from element idx,
+// idx a multiple of W, as float32.
+template <int W>
+__device__ __forceinline__ void load_values(const void* p, int dtype, int64_t idx, float (&v)[W]) {
+  static_assert(W == 4 || W == 8, "4 or 8 values");
+  if (dtype == 0) {
+    uint32_t w[W / 2];
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + idx;
+    if constexpr (W == 8) {
+      const v4i t = gload<v4i>(q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)t[i];
+    } else {
+      const v2u t = gload<v2u>(q);
+      w[0] = t[0];
+      w[1] = t[1];
+    }
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+    const float* q = reinterpret_cast<const float*>(p) + idx;
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const v4f t = gload<v4f>(q + 4 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = t[j];
+    }
+  }
+}
+
+// W consecutive outputs of row m from column n.
+template <int W>
+__device__ __forceinline__ void epilogue_values(const Epilogue& e, int64_t m, int64_t n, float (&v)[W]) {
+  if (e.bias != nullptr) {
+    float b[W];
+    load_values<W>(e.bias, e.bias_dtype, n, b);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += b[i];
+  }
+  activate<W>(e.act, v);
+  if (e.residual != nullptr) {
+    float r[W];
+    load_values<W>(e.residual, e.residual_dtype, m * e.ldr + n, r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += r[i];
+  }
+}
+
+// Store four consecutive outputs of one token, with the epilogue where the launch has one.
+template <int OUT, typename Args>
+__device__ __forceinline__ void store_out(const Args& p, int64_t m, int64_t n, v4f a) {
+  if constexpr (Args::kEpilogue) {
+    float v[4] = {a[0], a[1], a[2], a[3]};
+    epilogue_values<4>(p.ep, m, n, v);
+    a = v4f{v[0], v[1], v[2], v[3]};
+  }
+  store4<OUT>(p.y, p.ldy, m, n, a);
+}
+
+}  // namespace fgb

@@ -3,15 +3,9 @@
 // allocate.
 #include <mutex>
 
-#include "gemm_decode_kernels.hpp"
+#include "gemm_decode_launch.hpp"
 
 namespace fgb {
-
-namespace {
-
-int small_waves(int64_t N, int64_t K) { return decode_small_waves(N, K); }
-
-}  // namespace
 
 // Waves splitting K per 16-row tile in the M <= 16 kernels: 8 for at most 256 tiles (one per CU),
 // else 4 (and at most one per K-block).  Measured over the decode shapes at M = 1 and 8 (graph
@@ -80,101 +74,7 @@ size_t decode_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_gemm_decode(const GemmArgs& a, void* workspace, hipStream_t stream) {
-  if (a.M <= 16 && decode_ring(a.N, a.K)) {
-    const int wk = small_waves(a.N, a.K);
-    const dim3 grid((unsigned)(a.N / 16));
-#define FGB_RING(WK, SWF, OUT)                                                                              \
-  do {                                                                                                      \
-    if (a.M <= 8) hipLaunchKernelGGL((gemm_decode_ring_kernel<WK, 8, 5, SWF, OUT>), grid, dim3(64 * WK), 0, stream, a); \
-    else hipLaunchKernelGGL((gemm_decode_ring_kernel<WK, 16, 4, SWF, OUT>), grid, dim3(64 * WK), 0, stream, a);         \
-  } while (0)
-#define FGB_RING_WK(SWF, OUT)                  \
-  do {                                         \
-    if (wk == 1) FGB_RING(1, SWF, OUT);        \
-    else if (wk == 2) FGB_RING(2, SWF, OUT);   \
-    else if (wk == 4) FGB_RING(4, SWF, OUT);   \
-    else FGB_RING(8, SWF, OUT);                \
-  } while (0)
-    if (a.s_w_fmt == 0) {
-      if (a.y_dtype == 0) FGB_RING_WK(0, 0); else FGB_RING_WK(0, 1);
-    } else {
-      if (a.y_dtype == 0) FGB_RING_WK(1, 0); else FGB_RING_WK(1, 1);
-    }
-#undef FGB_RING_WK
-#undef FGB_RING
-    return hipGetLastError();
-  }
-  if (a.M > 16 && a.M <= 64 && ring_mid_rows(a.N, a.K)) {
-    const dim3 grid((unsigned)(a.N / 16));
-#define FGB_RING_MID(SWF, OUT)                                                                                   \
-  do {                                                                                                           \
-    if (a.M <= 32) hipLaunchKernelGGL((gemm_decode_ring_kernel<4, 32, 3, SWF, OUT>), grid, dim3(256), 0, stream, a); \
-    else hipLaunchKernelGGL((gemm_decode_ring_kernel<4, 64, 2, SWF, OUT>), grid, dim3(256), 0, stream, a);           \
-  } while (0)
-    if (a.s_w_fmt == 0) {
-      if (a.y_dtype == 0) FGB_RING_MID(0, 0); else FGB_RING_MID(0, 1);
-    } else {
-      if (a.y_dtype == 0) FGB_RING_MID(1, 0); else FGB_RING_MID(1, 1);
-    }
-#undef FGB_RING_MID
-    return hipGetLastError();
-  }
-  if (a.M <= 16) {
-    const int wk = small_waves(a.N, a.K);
-    const dim3 grid((unsigned)(a.N / 16));
-#define FGB_SMALL(WK, SWF, OUT) \
-  hipLaunchKernelGGL((gemm_decode_small_kernel<WK, SWF, OUT>), grid, dim3(64 * WK), 0, stream, a)
-#define FGB_SMALL_WK(SWF, OUT)                  \
-  do {                                          \
-    if (wk == 1) FGB_SMALL(1, SWF, OUT);        \
-    else if (wk == 2) FGB_SMALL(2, SWF, OUT);   \
-    else if (wk == 4) FGB_SMALL(4, SWF, OUT);   \
-    else FGB_SMALL(8, SWF, OUT);                \
-  } while (0)
-    if (a.s_w_fmt == 0) {
-      if (a.y_dtype == 0) FGB_SMALL_WK(0, 0); else FGB_SMALL_WK(0, 1);
-    } else {
-      if (a.y_dtype == 0) FGB_SMALL_WK(1, 0); else FGB_SMALL_WK(1, 1);
-    }
-#undef FGB_SMALL_WK
-#undef FGB_SMALL
-    return hipGetLastError();
-  }
-  {
-    const int S = decode_splits(a.M, a.N, a.K);
-    const int nw = mid_waves(a.M, a.N, a.K);
-    const int kpw = S == 1 ? (int)(a.K / 128) : mid_kpw(a.N, a.K);
-    const dim3 grid((unsigned)((a.N / (16 * nw)) * S)), block(64 * nw);
-    float* ws = reinterpret_cast<float*>(workspace);
-#define FGB_MID(NW_, MT_, D_, SWF, OUT) \
-  hipLaunchKernelGGL((gemm_decode_mid_kernel<NW_, MT_, D_, SWF, OUT>), grid, block, 0, stream, a, kpw, S, ws)
-#define FGB_MID_MT(SWF, OUT)                                    \
-  do {                                                          \
-    if (a.M > 64) FGB_MID(8, 8, kMidStages, SWF, OUT);          \
-    else if (a.M > 32) FGB_MID(8, 4, kMidStages, SWF, OUT);     \
-    else if (nw == 2) FGB_MID(2, 2, 6, SWF, OUT);               \
-    else if (nw == 4) FGB_MID(4, 2, 4, SWF, OUT);               \
-    else FGB_MID(8, 2, kMidStages, SWF, OUT);                   \
-  } while (0)
-    if (a.s_w_fmt == 0) {
-      if (a.y_dtype == 0) FGB_MID_MT(0, 0); else FGB_MID_MT(0, 1);
-    } else {
-      if (a.y_dtype == 0) FGB_MID_MT(1, 0); else FGB_MID_MT(1, 1);
-    }
-#undef FGB_MID_MT
-#undef FGB_MID
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess || S == 1) return err;
-    const int64_t total = a.M * (a.N / 4);
-    const dim3 rgrid((unsigned)((total + 255) / 256));
-    if (a.y_dtype == 0)
-      hipLaunchKernelGGL(splitk_reduce_kernel<0>, rgrid, dim3(256), 0, stream, ws, S, a.M, a.N, a.y, a.ldy,
-                         nullptr, 0, nullptr);
-    else
-      hipLaunchKernelGGL(splitk_reduce_kernel<1>, rgrid, dim3(256), 0, stream, ws, S, a.M, a.N, a.y, a.ldy,
-                         nullptr, 0, nullptr);
-    return hipGetLastError();
-  }
+  return launch_decode_kernels(a, workspace, stream);
 }
 
 // ---------------------------------------------------------------------------------------------

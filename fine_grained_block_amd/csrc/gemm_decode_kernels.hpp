@@ -29,6 +29,7 @@
 #pragma once
 #include <type_traits>
 
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "internal.h"
 #include "quant_common.hpp"
@@ -48,16 +49,7 @@ __device__ __forceinline__ int swz(int row, int chunk) {
 // before they are added.  SCH 1 and 2 (scales that do not vary along K, see the ring kernel)
 // then multiply by the token's or the tensor's activation scale s_a (a_kind 1 or 2) and, for
 // SCH 2, by the channels' weight scales s_w[n .. n+3].
-template <int OUT, int SCH = 0>
-__global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ ws, int S, int64_t M,
-                                                            int64_t N, void* y, int64_t ldy, const float* s_a,
-                                                            int a_kind, const float* s_w) {
-  const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // one float4 of y
-  const int64_t total = M * (N / 4);
-  if (q >= total) return;
-  const int64_t m = q / (N / 4), n = (q - m * (N / 4)) * 4;
-  const float* base = ws + m * N + n;
-  const int64_t slice = M * N;
+__device__ __forceinline__ v4f splitk_sum(const float* base, int S, int64_t slice) {
   v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i0 = 0; i0 < S; i0 += 8) {
     v4f v[8];
@@ -69,11 +61,34 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restr
       if (i0 + u < S) s += v[u];
     }
   }
+  return s;
+}
+
+template <int OUT, int SCH = 0>
+__global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ ws, int S, int64_t M,
+                                                            int64_t N, void* y, int64_t ldy, const float* s_a,
+                                                            int a_kind, const float* s_w) {
+  const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // one float4 of y
+  const int64_t total = M * (N / 4);
+  if (q >= total) return;
+  const int64_t m = q / (N / 4), n = (q - m * (N / 4)) * 4;
+  v4f s = splitk_sum(ws + m * N + n, S, M * N);
   if constexpr (SCH != 0) {
     s = s * gload<float>(s_a + (a_kind == 2 ? 0 : m));
     if constexpr (SCH == 2) s = s * gload<v4f>(s_w + n);
   }
   store4<OUT>(y, ldy, m, n, s);
+}
+
+// The same ordered sum, then the epilogue of the whole sum (each thread reads the residual elements
+// that it writes, so the residual may be y itself).
+template <int OUT>
+__global__ __launch_bounds__(256) void splitk_reduce_epilogue_kernel(const float* __restrict__ ws, int S,
+                                                                     GemmEpiArgs p) {
+  const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (q >= p.M * (p.N / 4)) return;
+  const int64_t m = q / (p.N / 4), n = (q - m * (p.N / 4)) * 4;
+  store_out<OUT>(p, m, n, splitk_sum(ws + m * p.N + n, S, p.M * p.N));
 }
 
 #define GPTR(p) ((const void __attribute__((address_space(1)))*)(p))
@@ -101,8 +116,8 @@ __device__ __forceinline__ int swz_g(int row) { return (row & 7) ^ ((row >> 3) &
 // per-channel weight scales and per-token or per-tensor activation scales, both in the epilogue
 // (the MFMAs accumulate in place).  CODE 1: E5M2 operands (schemes 1 and 2).
 //
-template <int WK, int MR, int D, int SWF, int OUT, int SCH = 0, int CODE = 0>
-__global__ __launch_bounds__(64 * WK) void gemm_decode_ring_kernel(GemmArgs p) {
+template <int WK, int MR, int D, int SWF, int OUT, int SCH = 0, int CODE = 0, typename Args = GemmArgs>
+__global__ __launch_bounds__(64 * WK) void gemm_decode_ring_kernel(Args p) {
   static_assert(SCH != 0 || CODE == 0, "the 1x128-group scheme runs on E4M3 operands");
   constexpr int MT = MR >= 16 ? MR / 16 : 1;  // token tiles per wave
   constexpr int WST = 16 * 128, AST = MR * 128, SST = 64 * 4;
@@ -302,7 +317,7 @@ __global__ __launch_bounds__(64 * WK) void gemm_decode_ring_kernel(GemmArgs p) {
           acc[j] = acc[j] * gload<float>(p.s_a + (p.a_kind == 2 ? 0 : m));
           if constexpr (SCH == 2) acc[j] = acc[j] * gload<v4f>(reinterpret_cast<const float*>(p.s_w) + n0 + 4 * (lane >> 4));
         }
-        store4<OUT>(p.y, p.ldy, m, n0 + 4 * (lane >> 4), acc[j]);
+        store_out<OUT>(p, m, n0 + 4 * (lane >> 4), acc[j]);
       }
     }
   };
@@ -536,8 +551,8 @@ __global__ __launch_bounds__(64 * WK) void gemm_decode_fused_quant_small_kernel(
 // SCH and CODE as for the ring kernel (schemes 1 and 2 copy no activation scales; their scales
 // that do not vary along K multiply the finished sums, here or in the reduction).
 // ---------------------------------------------------------------------------------------------
-template <int NW, int MT, int D, int SWF, int OUT, int SCH = 0, int CODE = 0>
-__global__ __launch_bounds__(64 * NW, 1) void gemm_decode_mid_kernel(GemmArgs p, int kpw, int S, float* ws) {
+template <int NW, int MT, int D, int SWF, int OUT, int SCH = 0, int CODE = 0, typename Args = GemmArgs>
+__global__ __launch_bounds__(64 * NW, 1) void gemm_decode_mid_kernel(Args p, int kpw, int S, float* ws) {
   static_assert(SCH != 0 || CODE == 0, "the 1x128-group scheme runs on E4M3 operands");
   static_assert(NW == 2 || NW == 4 || NW == 8, "2, 4 or 8 waves");
   constexpr int MROWS = 16 * MT;
@@ -736,7 +751,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_decode_mid_kernel(GemmArgs p,
           acc[j] = acc[j] * gload<float>(p.s_a + (p.a_kind == 2 ? 0 : m));
           if constexpr (SCH == 2) acc[j] = acc[j] * gload<v4f>(reinterpret_cast<const float*>(p.s_w) + n);
         }
-        store4<OUT>(p.y, p.ldy, m, n, acc[j]);
+        store_out<OUT>(p, m, n, acc[j]);
       } else {
         gstore<v4f>(ws + ((int64_t)split * M + m) * N + n, acc[j]);
       }
@@ -770,8 +785,8 @@ constexpr int CHS = 2;  // K-blocks per register chunk in the small-M kernel (4:
 // (MoE layouts: scheme 0 only).
 // (at least 3 waves per SIMD: with both pass variants of the MoE walk, the 16-row form would
 // otherwise take 172 VGPRs and run 2 waves per SIMD, 13-25% slower on MoE down)
-template <int WK, int SWF, int OUT, int MODE = 0, int SCH = 0, int CODE = 0, int MT_MAX = 1>
-__global__ __launch_bounds__(64 * WK, 3) void gemm_decode_small_kernel(GemmArgs p) {
+template <int WK, int SWF, int OUT, int MODE = 0, int SCH = 0, int CODE = 0, int MT_MAX = 1, typename Args = GemmArgs>
+__global__ __launch_bounds__(64 * WK, 3) void gemm_decode_small_kernel(Args p) {
   static_assert(SCH != 0 || CODE == 0, "the 1x128-group scheme runs on E4M3 operands");
   static_assert(MODE == 0 || SCH == 0, "MoE layouts use the 1x128-group scheme");
   static_assert(MT_MAX == 1 || MT_MAX == 2, "16-row tiles per pass: 1 or 2");
@@ -894,7 +909,7 @@ __global__ __launch_bounds__(64 * WK, 3) void gemm_decode_small_kernel(GemmArgs 
           acc[t] = acc[t] * gload<float>(p.s_a + (p.a_kind == 2 ? 0 : row_base + ml));
           if constexpr (SCH == 2) acc[t] = acc[t] * gload<v4f>(reinterpret_cast<const float*>(p.s_w) + n0 + 4 * g);
         }
-        store4<OUT>(p.y, p.ldy, row_base + ml, n0 + 4 * g, acc[t]);
+        store_out<OUT>(p, row_base + ml, n0 + 4 * g, acc[t]);
       }
     };
     if constexpr (WK > 1) {

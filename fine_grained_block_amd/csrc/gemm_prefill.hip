@@ -5,32 +5,9 @@
 // fill whole waves of CUs; with more 256 x 256 tiles than CUs and a short K (grouped: up to 64
 // K-blocks) one workgroup per CU walks the tiles (gemm_prefill_persistent_kernel) and overlaps
 // the work between consecutive tiles.
-#include "gemm_prefill_kernels.hpp"
+#include "gemm_prefill_launch.hpp"
 
 namespace fgb {
-
-namespace {
-
-
-template <typename C, bool GROUPED>
-hipError_t launch_cfg(const GemmArgs& a, int tiles_m, hipStream_t stream) {
-  const int tiles_n = (int)(a.N / C::BN);
-  // grouped: tiles_m is an upper bound; a multiple of 8 workgroups gives every XCD at least its
-  // share of the real tiles
-  const int nwg = GROUPED ? (tiles_m * tiles_n + 7) / 8 * 8 : tiles_m * tiles_n;
-  dim3 grid(nwg), block(C::THREADS);
-#define FGB_LAUNCH(SWF, OUT)                                                                  \
-  hipLaunchKernelGGL((gemm_prefill_kernel<C, SWF, OUT, GROUPED>), grid, block, 0, stream, a, \
-                     tiles_m, tiles_n)
-  if (a.s_w_fmt == 0 && a.y_dtype == 0) FGB_LAUNCH(0, 0);
-  else if (a.s_w_fmt == 0) FGB_LAUNCH(0, 1);
-  else if (a.y_dtype == 0) FGB_LAUNCH(1, 0);
-  else FGB_LAUNCH(1, 1);
-#undef FGB_LAUNCH
-  return hipGetLastError();
-}
-
-}  // namespace
 
 // Compute units of the current device (cached per device).
 int cu_count() {
@@ -45,25 +22,6 @@ int cu_count() {
   return cached[dev];
 }
 
-namespace {
-
-template <typename C>
-int64_t tiles_for(int64_t M, int64_t N) { return ((M + C::BM - 1) / C::BM) * (N / C::BN); }
-
-// The persistent form for more 256 x 256 tiles than CUs when K has at most max_kb blocks.  Dense
-// (16 blocks), where the work between tiles weighs most: measured +4-7% at 12-16 blocks; at 32
-// (gate+up) +2% alone but 0.5% slower inside the Llama step, and 0.2-1.5% slower at 56-144
-// blocks.  Grouped (64 blocks): a one-tile launch also looks up each tile's expert when it
-// starts, which the persistent form does from registers; MoE gate+up (56 blocks) +2-4%.  An even
-// K-block count (a multiple of 4 with UE8M0 scales, copied four to a dword), bf16 output and
-// 32-bit output offsets.
-bool use_persistent(const GemmArgs& a, int64_t max_kb) {
-  const int64_t KB = a.K / KBYTES, tiles = tiles_for<Big>(a.M, a.N);
-  return tiles > cu_count() && KB <= max_kb && KB % 2 == 0 && (a.s_w_fmt == 0 || KB % 4 == 0) && a.y_dtype == 0 &&
-         a.M * a.ldy * 2 < (int64_t(1) << 32);
-}
-
-
 // Tile choice (N % 256 == 0; otherwise 128 x 128 tiles with 2 stages).  256 x 256 tiles (8 waves
 // of 128 x 64, two stages) need K of at least 8 blocks; 256 x 128 tiles (three stages, 8 waves of
 // 64 x 64: four token tiles per wave, so the pinned MFMA/FMA pipeline applies) take ~0.6 of a
@@ -72,8 +30,6 @@ bool use_persistent(const GemmArgs& a, int64_t max_kb) {
 // own launch, with n_big chosen to minimize the waves of tiles over the CUs (one tile per CU at
 // a time), weighted 1 and 0.6.  Whole waves of big tiles plus one wave of half tiles can beat
 // either tile alone: QKV at M = 4096 (384 big tiles) runs 256 big + 256 half tiles.
-}  // namespace
-
 int64_t big_columns(int64_t M, int64_t N, int64_t K) {
   if (K < 8 * KBYTES) return 0;
   const int64_t cus = cu_count(), nc = N / Big::BN;
@@ -138,50 +94,17 @@ hipError_t launch_sliced(const GemmArgs& a, int S, float* ws, hipStream_t stream
     hipLaunchKernelGGL((gemm_prefill_kernel<C, 0, 1, false, 0, 0, true>), grid, block, 0, stream, b, tiles_m, tiles_n);
   else
     hipLaunchKernelGGL((gemm_prefill_kernel<C, 1, 1, false, 0, 0, true>), grid, block, 0, stream, b, tiles_m, tiles_n);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_splitk_reduce(ws, S, a.M, a.N, a.y, a.y_dtype, a.ldy, stream);
+  return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t launch_prefill_slices(const GemmArgs& a, int S, float* ws, hipStream_t stream) {
+  return a.N % Half::BN == 0 ? launch_sliced<Half>(a, S, ws, stream) : launch_sliced<Narrow>(a, S, ws, stream);
+}
+
 hipError_t launch_gemm_prefill(const GemmArgs& a, void* workspace, hipStream_t stream) {
-  const int S = prefill_splits(a.M, a.N, a.K);
-  if (S > 1) {
-    float* ws = reinterpret_cast<float*>(workspace);
-    return a.N % Half::BN == 0 ? launch_sliced<Half>(a, S, ws, stream) : launch_sliced<Narrow>(a, S, ws, stream);
-  }
-  if (a.N % Big::BN != 0 || a.N % Half::BN != 0)
-    return launch_cfg<Narrow, false>(a, (int)((a.M + Narrow::BM - 1) / Narrow::BM), stream);
-  const int64_t n_big = big_columns(a.M, a.N, a.K);
-  if (n_big > 0) {
-    GemmArgs b = a;
-    b.N = n_big;
-    const int tiles_m = (int)((b.M + Big::BM - 1) / Big::BM);
-    if (use_persistent(b, 16)) {
-      // one workgroup per CU (a multiple of 8, as the XCD mapping of tiles assumes)
-      const dim3 grid(cu_count() / 8 * 8);
-      if (b.s_w_fmt == 0)
-        hipLaunchKernelGGL((gemm_prefill_persistent_kernel<Big, 0, false>), grid, dim3(Big::THREADS), 0, stream, b,
-                           tiles_m, (int)(b.N / Big::BN));
-      else
-        hipLaunchKernelGGL((gemm_prefill_persistent_kernel<Big, 1, false>), grid, dim3(Big::THREADS), 0, stream, b,
-                           tiles_m, (int)(b.N / Big::BN));
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    } else {
-      const hipError_t e = launch_cfg<Big, false>(b, tiles_m, stream);
-      if (e != hipSuccess) return e;
-    }
-  }
-  if (n_big == a.N) return hipSuccess;
-  // the remaining output columns: their weight rows, block-scale rows and output columns
-  GemmArgs h = a;
-  h.N = a.N - n_big;
-  h.w_q = a.w_q + n_big * a.K;
-  h.s_w = (const uint8_t*)a.s_w + (n_big / 128) * (a.K / KBYTES) * (a.s_w_fmt == 0 ? 4 : 1);
-  h.y = (uint8_t*)a.y + n_big * (a.y_dtype == 0 ? 2 : 4);
-  return launch_cfg<Half, false>(h, (int)((h.M + Half::BM - 1) / Half::BM), stream);
+  return launch_prefill_kernels(a, workspace, stream);
 }
 
 hipError_t launch_gemm_grouped(const GemmArgs& a, hipStream_t stream) {

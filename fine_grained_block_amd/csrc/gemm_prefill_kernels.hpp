@@ -31,6 +31,7 @@
 // and a short K (grouped: up to 64 K-blocks) one workgroup per CU walks the tiles
 // (gemm_prefill_persistent_kernel) and overlaps the work between consecutive tiles.
 #pragma once
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "internal.h"
 
@@ -112,8 +113,11 @@ __device__ __forceinline__ v8i lds_frag(const uint8_t* base, int row0, int lane)
 // operands' format (0 E4M3, 1 E5M2; schemes 1 and 2 only).  SPLIT: K-sliced launch (dense, scheme
 // 0, float32 output): workgroup (x, y) multiplies tile x over K-blocks y*kslice ..
 // min((y+1)*kslice, K/128) - 1 and writes its float32 partial tile to slice y of y = [S][M][ldy].
-template <typename C, int SWF, int OUT, bool GROUPED, int SCH = 0, int CODE = 0, bool SPLIT = false>
-__global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(GemmArgs p, int tiles_m, int tiles_n) {
+// Args: GemmArgs, or GemmEpiArgs for the dense GEMM with an epilogue (scheme 0, K whole).
+template <typename C, int SWF, int OUT, bool GROUPED, int SCH = 0, int CODE = 0, bool SPLIT = false,
+          typename Args = GemmArgs>
+__global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args p, int tiles_m, int tiles_n) {
+  static_assert(!Args::kEpilogue || (!GROUPED && SCH == 0 && !SPLIT), "epilogue: dense block scheme, K whole");
   static_assert(!SPLIT || (!GROUPED && SCH == 0 && OUT == 1), "K slices: dense block scheme, float32 partials");
   static_assert(SCH == 0 || SCH == 1 || SCH == 2, "scheme");
   static_assert(SCH != 0 || CODE == 0, "the 1x128-group scheme runs on E4M3 operands");
@@ -462,6 +466,103 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(GemmA
         if constexpr (SCH == 2) acc[i][j] = acc[i][j] * ew;
       }
     }
+  }
+
+  if constexpr (Args::kEpilogue) {
+    // The float32 sums go through LDS (all stages, free once every wave is past its last block),
+    // so that each thread finishes 8 consecutive outputs of a row: one 16-byte residual load and
+    // one 16-byte store per bf16 group, whole lines per wave, and the activation once per value in
+    // a thread whose column group, hence bias, is the same in every iteration.  Staged as float32
+    // because y is rounded once, after the residual is added.  16-byte chunk c of row r sits at
+    // c ^ (r & 15): the 16 rows of a fragment write to distinct banks.
+    constexpr int ROWF = C::BN * 4;
+    constexpr int RPS = C::STAGE / ROWF / 16 * 16;                             // rows per stage
+    constexpr int RPR = RPS * C::STAGES < C::BM ? RPS * C::STAGES : C::BM;     // rows per round
+    constexpr int CPR = C::BN / 8;                                             // 8-column groups per row
+    constexpr int NIT = RPR * CPR / C::THREADS;                                // groups per thread per round
+    static_assert(RPS >= 16 && C::BM % RPR == 0 && C::THREADS % CPR == 0, "whole rounds, fixed columns per thread");
+    auto staged_row = [&](int rr) -> uint8_t* {
+      const int s = rr / RPS;
+      uint8_t* const base = s == 0 ? stage0 : (s == 1 ? stage1 : stage2);
+      return base + (rr - s * RPS) * ROWF;
+    };
+    const int ch = tid % CPR, mr0 = tid / CPR;
+    const int64_t ncol = n0 + ch * 8;
+    float bias[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.ep.bias != nullptr) load_values<8>(p.ep.bias, p.ep.bias_dtype, ncol, bias);
+    const bool res16 = p.ep.residual != nullptr && p.ep.residual_dtype == 0;
+    const bool res32 = p.ep.residual != nullptr && p.ep.residual_dtype != 0;
+    const int wrow = wm * (C::BM / C::WM);
+#pragma unroll
+    for (int r = 0; r < C::BM / RPR; ++r) {
+      // this round's bf16 residual goes out before the barriers (float32 residuals, twice the
+      // registers, are loaded where they are added)
+      v4i res[NIT];
+      if (res16) {
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+          int64_t m = row0 + r * RPR + mr0 + it * (C::THREADS / CPR);
+          m = m < row_end ? m : row_end - 1;
+          res[it] = gload<v4i>(reinterpret_cast<const uint16_t*>(p.ep.residual) + m * p.ep.ldr + ncol);
+        }
+      }
+      wg_barrier();  // every wave is past its last block, or past the reads of the previous round
+#pragma unroll
+      for (int j = 0; j < C::TM; ++j) {
+        if ((wrow + j * 16) / RPR == r) {  // (wave-uniform)
+          uint8_t* const frag = staged_row((wrow + j * 16) % RPR) + (lane & 15) * ROWF;
+#pragma unroll
+          for (int i = 0; i < C::TN; ++i) {
+            const int c = (wn * (C::BN / C::WN) + i * 16) / 4 + (lane >> 4);
+            *reinterpret_cast<v4f*>(frag + ((c ^ (lane & 15)) << 4)) = acc[i][j];
+          }
+        }
+      }
+      wg_barrier_after_lds_writes();
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) {
+        const int mr = mr0 + it * (C::THREADS / CPR);
+        const int64_t m = row0 + r * RPR + mr;
+        if (m < row_end) {
+          // (lanes 8..15 of 16 take their two chunks in the other order: the 16 lanes served
+          // together then read 16 distinct bank groups)
+          const uint8_t* const row = staged_row(mr);
+          const int odd = (ch >> 3) & 1;
+          const v4f x0 = *reinterpret_cast<const v4f*>(row + (((2 * ch + odd) ^ (mr & 15)) << 4));
+          const v4f x1 = *reinterpret_cast<const v4f*>(row + (((2 * ch + 1 - odd) ^ (mr & 15)) << 4));
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] = (odd ? x1[q] : x0[q]) + bias[q];
+            v[4 + q] = (odd ? x0[q] : x1[q]) + bias[4 + q];
+          }
+          activate<8>(p.ep.act, v);
+          if (res16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[2 * q] += bf16_lo((uint32_t)res[it][q]);
+              v[2 * q + 1] += bf16_hi((uint32_t)res[it][q]);
+            }
+          } else if (res32) {
+            float f[8];
+            load_values<8>(p.ep.residual, 1, m * p.ep.ldr + ncol, f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += f[q];
+          }
+          if constexpr (OUT == 0) {
+            v4i w;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = (int)pack_bf16x2(v[2 * q], v[2 * q + 1]);
+            __builtin_nontemporal_store(w, reinterpret_cast<v4i*>(reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + ncol));
+          } else {
+            float* const yp = reinterpret_cast<float*>(p.y) + m * p.ldy + ncol;
+            __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, reinterpret_cast<v4f*>(yp));
+            __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]}, reinterpret_cast<v4f*>(yp + 4));
+          }
+        }
+      }
+    }
+    return;
   }
 
   // epilogue.  bf16 tiles go through LDS in rounds of two 64-row chunks (stage0 and stage1, free

@@ -23,6 +23,7 @@ hipError_t launch_selftest_quotients(unsigned long long* counts, hipStream_t str
 
 // Block-scaled GEMM problem description (dense or grouped).
 struct GemmArgs {
+  static constexpr bool kEpilogue = false;
   const uint8_t* a_q;
   int64_t lda;
   const float* s_a;
@@ -47,12 +48,29 @@ struct GemmArgs {
   int kslice;
 };
 
+// Epilogue of a dense GEMM: y = act(sum + bias) + residual (bias and residual may be absent).
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;
+struct Epilogue {
+  const void* bias;  // [N], 16-byte aligned
+  int bias_dtype;    // 0 bf16, 1 float32
+  int act;
+  const void* residual;  // [M, ldr]; may be y itself (same type and pitch)
+  int residual_dtype;
+  int64_t ldr;
+};
+struct GemmEpiArgs : GemmArgs {
+  static constexpr bool kEpilogue = true;
+  Epilogue ep;
+};
+
 // Prefill (M > 64) dense GEMM and the grouped variant.  Launches with too few output tiles to
 // occupy the CUs (M a little above the decode sizes, narrow N) slice K: float32 partials in
 // `workspace` (prefill_workspace_bytes), added in slice order by a second launch.
 int prefill_splits(int64_t M, int64_t N, int64_t K);
 size_t prefill_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_prefill(const GemmArgs& a, void* workspace, hipStream_t stream);
+// the S K-slices' float32 partial tiles of a into ws = [S][M][N]
+hipError_t launch_prefill_slices(const GemmArgs& a, int S, float* ws, hipStream_t stream);
 // y[m, n] = sum over s of ws[s][m][n] in slice order, as bf16 (y_dtype 0) or float32
 hipError_t launch_splitk_reduce(const float* ws, int S, int64_t M, int64_t N, void* y, int y_dtype, int64_t ldy,
                                 hipStream_t stream);
@@ -103,6 +121,13 @@ int mid_waves(int64_t M, int64_t N, int64_t K);
 int decode_splits(int64_t M, int64_t N, int64_t K);
 size_t decode_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_decode(const GemmArgs& a, void* workspace, hipStream_t stream);
+
+// The dense GEMM with an epilogue: the launches of launch_gemm_decode and launch_gemm_prefill
+// (same kernel selection and workspace plan).
+hipError_t launch_gemm_epilogue_decode(const GemmEpiArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_gemm_epilogue_prefill(const GemmEpiArgs& a, void* workspace, hipStream_t stream);
+// the ordered sum of the K slices' partials, then the epilogue
+hipError_t launch_splitk_reduce_epilogue(const float* ws, int S, const GemmEpiArgs& a, hipStream_t stream);
 
 // Scratch that the library owns for callers that cannot allocate: kScratchBytes per GPU.  It
 // covers every workspace of the GEMM: the decode plans need at most 128 x 49024 float32 partials

@@ -12,8 +12,9 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import (ACT_SCALE_TENSOR, ACT_SCALE_TOKEN, FP8_E4M3, FP8_E5M2, OUT_BF16, OUT_F32, SCALE_F32,
-                   SCALE_UE8M0, W_SCALE_BLOCK128, W_SCALE_CHANNEL, check, lib)
+from ._lib import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SCALE_TENSOR, ACT_SCALE_TOKEN, ACT_SILU,
+                   FP8_E4M3, FP8_E5M2, OUT_BF16, OUT_F32, SCALE_F32, SCALE_UE8M0, W_SCALE_BLOCK128, W_SCALE_CHANNEL,
+                   check, lib)
 
 BLOCK = 128
 
@@ -321,6 +322,48 @@ def gemm_noalloc(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: t
                                            _ptr(s_w), _scale_fmt(s_w), _ptr(out), _out_code(out.dtype),
                                            _row_ld(out), M, N, K, _stream())
     check("fgb_w8a8_block_gemm_noalloc", st)
+    return out
+
+
+_ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+_VALUES = (torch.bfloat16, torch.float32)
+
+
+def gemm_epilogue(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor,
+                  bias: torch.Tensor | None = None, activation: str = "none",
+                  residual: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = act(gemm(a_q, s_a, w_q, s_w) + bias) + residual, in float32, rounded once to `out`'s type.
+
+    Operands, out and workspace as for gemm(); bias [N] and residual [M, N] (unit inner stride) are
+    bf16 or float32; activation is "none", "relu", "gelu" (erf), "gelu_tanh" or "silu".  `out` may be
+    the residual tensor itself (y += ...).
+    """
+    M, N, K = _check_gemm_operands(a_q, s_a, w_q, s_w, out, None)
+    act = _ACTIVATIONS.get(activation)
+    _need(act is not None, f"activation must be one of {tuple(_ACTIVATIONS)}")
+    if bias is not None:
+        _dense(bias, "bias", _VALUES, (N,))
+    if residual is not None:
+        _need(isinstance(residual, torch.Tensor) and residual.dtype in _VALUES, "residual must be bf16 or float32")
+        _matrix(residual, "residual", residual.dtype, rows=M, cols=N)
+    if workspace is not None:
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
+    _on_device(("a_q", a_q), ("s_a", s_a), ("w_q", w_q), ("s_w", s_w), ("bias", bias), ("residual", residual),
+               ("out", out), ("workspace", workspace))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
+    need = gemm_workspace_bytes(M, N, K)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().fgb_w8a8_block_gemm_epilogue(
+        _ptr(a_q), _row_ld(a_q), _ptr(s_a), s_a.stride(0), _ptr(w_q), _ptr(s_w), _scale_fmt(s_w),
+        _ptr(bias), 0 if bias is None else _out_code(bias.dtype), act,
+        _ptr(residual), 0 if residual is None else _out_code(residual.dtype),
+        0 if residual is None else _row_ld(residual), _ptr(out), _out_code(out.dtype), _row_ld(out), M, N, K,
+        _ptr(workspace), ws_bytes, _stream())
+    check("fgb_w8a8_block_gemm_epilogue", st)
     return out
 
 

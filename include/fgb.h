@@ -71,6 +71,16 @@ typedef enum {
   FGB_W_SCALE_CHANNEL = 1   /* one scale per output feature (row of W), float32 [N] */
 } fgb_w_scale;
 
+/* Activation of fgb_w8a8_block_gemm_epilogue and of the experts of fgb_moe_ffn (gated there; NONE and
+ * RELU are not experts' activations).  gelu(v) = v Phi(v); gelu_tanh its tanh form; silu(v) = v / (1 + e^-v). */
+typedef enum {
+  FGB_ACT_NONE = 0,
+  FGB_ACT_RELU = 1,
+  FGB_ACT_GELU = 2,
+  FGB_ACT_GELU_TANH = 3,
+  FGB_ACT_SILU = 4
+} fgb_activation;
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* fgb_status_string(int status);
 
@@ -151,6 +161,26 @@ int fgb_w8a8_block_gemm_noalloc(const uint8_t* a_q, int64_t lda, const float* s_
                                 const uint8_t* w_q, const void* s_w, int s_w_fmt,
                                 void* y, int y_dtype, int64_t ldy,
                                 int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * fgb_w8a8_block_gemm with bias, activation and residual in its epilogue:
+ *   y[m, n] = act(sum[m, n] + bias[n]) + residual[m, n]
+ * in float32 on the float32 sum of fgb_w8a8_block_gemm, rounded once to y_dtype.  Operands, y, size
+ * limits, kernel selection and workspace (fgb_gemm_workspace_bytes) as for fgb_w8a8_block_gemm; with no
+ * bias, FGB_ACT_NONE and no residual the result is that call's.
+ *   bias      [N] bf16 or float32 per bias_dtype (fgb_out_dtype values), 16-byte aligned; NULL: none.
+ *   activation  fgb_activation.
+ *   residual  [M, ldr] bf16 or float32 per residual_dtype, 16-byte aligned rows, ldr >= N; NULL: none.
+ *             It may be y itself (same address, type and pitch: y += ...); other overlap with y is
+ *             not allowed.
+ * bias_dtype is ignored without a bias, residual_dtype and ldr without a residual.
+ */
+int fgb_w8a8_block_gemm_epilogue(const uint8_t* a_q, int64_t lda, const float* s_a, int64_t ld_sa,
+                                 const uint8_t* w_q, const void* s_w, int s_w_fmt,
+                                 const void* bias, int bias_dtype, int activation,
+                                 const void* residual, int residual_dtype, int64_t ldr,
+                                 void* y, int y_dtype, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* Host query: workspace bytes fgb_w8a8_block_gemm_fused_quant needs (0 if none, and for shapes it
  * rejects). */
