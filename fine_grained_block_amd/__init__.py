@@ -11,6 +11,8 @@ fallback: if the library is missing, or a call returns a nonzero status, an exce
     y = gemm(q, s_a, w_q, s_w)           # bf16 [M, N]
     y = grouped_gemm(q, s_a, w_q, s_w, offsets)
     y = gemm_epilogue(q, s_a, w_q, s_w, bias=b, activation="silu", residual=r)
+    ids, weights = moe_route(logits, top_k)
+    y = moe_ffn(x, ids, weights, w13_q, s_w13, w2_q, s_w2, residual=x)
 """
 from ._lib import (  # noqa: F401
     FGBError,
@@ -44,6 +46,9 @@ from .ops import (  # noqa: F401
     gemm_fused_quant_workspace_bytes,
     grouped_gemm,
     batched_gemm,
+    moe_route,
+    moe_ffn,
+    moe_ffn_workspace_bytes,
     check_offsets,
     gemm_workspace_bytes,
     fp8_encode,

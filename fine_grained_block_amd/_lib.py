@@ -12,6 +12,7 @@ ACT_SCALE_GROUP128, ACT_SCALE_TOKEN, ACT_SCALE_TENSOR = 0, 1, 2
 W_SCALE_BLOCK128, W_SCALE_CHANNEL = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 FP8_E4M3, FP8_E5M2, UE8M0, FP8_E4M3_INT = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 
 _c_i64 = ctypes.c_int64
@@ -40,6 +41,12 @@ _SIGS = {
     "fgb_batched_w8a8_block_gemm": (ctypes.c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _vp, ctypes.c_int, _vp,
                                                    ctypes.c_int32, _c_i64, _vp, ctypes.c_int, _c_i64, _c_i64,
                                                    _c_i64, _vp]),
+    "fgb_moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _c_i64, _c_i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
+                                     _vp, ctypes.c_int, ctypes.c_float, _vp, _vp, _vp]),
+    "fgb_moe_ffn_workspace_bytes": (ctypes.c_size_t, [_c_i64, ctypes.c_int32, ctypes.c_int32, _c_i64, _c_i64]),
+    "fgb_moe_ffn": (ctypes.c_int, [_vp, _c_i64, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, ctypes.c_int,
+                                   ctypes.c_int32, ctypes.c_int, _vp, ctypes.c_int, _c_i64, _vp, ctypes.c_int, _c_i64,
+                                   _c_i64, _c_i64, _c_i64, _vp, ctypes.c_size_t, _vp]),
     "fgb_check_expert_offsets": (ctypes.c_int, [_vp, ctypes.c_int32, _c_i64, _vp, _vp]),
     "fgb_act_quant_per_token": (ctypes.c_int, [_vp, _c_i64, _c_i64, _c_i64, ctypes.c_int, _vp, _c_i64, _vp, _vp]),
     "fgb_weight_quant_per_channel": (ctypes.c_int, [_vp, _c_i64, _c_i64, ctypes.c_int, _vp, _vp, _vp]),

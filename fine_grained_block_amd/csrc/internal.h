@@ -129,6 +129,46 @@ hipError_t launch_gemm_epilogue_prefill(const GemmEpiArgs& a, void* workspace, h
 // the ordered sum of the K slices' partials, then the epilogue
 hipError_t launch_splitk_reduce_epilogue(const float* ws, int S, const GemmEpiArgs& a, hipStream_t stream);
 
+// Router of a mixture of experts (moe_route.hip).
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 32;
+struct RouteArgs {
+  const void* logits;  // [T, ld]
+  int dtype;           // 0 bf16, 1 float32
+  int64_t ld, T;
+  int E, top_k;
+  int scoring;  // 0 softmax, 1 sigmoid
+  const float* bias;  // [E] added to the scores for the selection only, or null
+  int renorm;
+  float scale;
+  int32_t* ids;    // [T, top_k]
+  float* weights;  // [T, top_k]
+};
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
+
+// A whole mixture-of-experts layer for a few tokens (moe_ffn.hip).
+constexpr int kMoeMaxTokens = 64, kMoeMaxPairs = 1024, kMoeMaxExperts = 1024;
+struct MoeArgs {
+  const uint16_t* x;  // bf16 [T, ldx]
+  int64_t ldx;
+  const int32_t* ids;    // [T, top_k]
+  const float* weights;  // [T, top_k]
+  const uint8_t* w13_q;  // [E, 2I, H]: gate rows, then up rows
+  const void* s_w13;
+  const uint8_t* w2_q;  // [E, H, I]
+  const void* s_w2;
+  int s_w_fmt;
+  int act;
+  const void* residual;  // [T, ldr] or null
+  int residual_dtype;
+  int64_t ldr;
+  void* y;  // [T, ldy]
+  int y_dtype;
+  int64_t ldy;
+  int T, top_k, E, H, I;
+};
+size_t moe_ffn_workspace_bytes(int T, int top_k, int E, int H, int I);
+hipError_t launch_moe_ffn(const MoeArgs& a, void* workspace, hipStream_t stream);
+
 // Scratch that the library owns for callers that cannot allocate: kScratchBytes per GPU.  It
 // covers every workspace of the GEMM: the decode plans need at most 128 x 49024 float32 partials
 // (24.5 MiB), and the K-sliced prefill plan is capped at this size.

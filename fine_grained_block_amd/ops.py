@@ -13,8 +13,8 @@ from __future__ import annotations
 import torch
 
 from ._lib import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SCALE_TENSOR, ACT_SCALE_TOKEN, ACT_SILU,
-                   FP8_E4M3, FP8_E5M2, OUT_BF16, OUT_F32, SCALE_F32, SCALE_UE8M0, W_SCALE_BLOCK128, W_SCALE_CHANNEL,
-                   check, lib)
+                   FP8_E4M3, FP8_E5M2, OUT_BF16, OUT_F32, SCALE_F32, SCALE_UE8M0, SCORE_SIGMOID, SCORE_SOFTMAX,
+                   W_SCALE_BLOCK128, W_SCALE_CHANNEL, check, lib)
 
 BLOCK = 128
 
@@ -409,6 +409,104 @@ def batched_gemm(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: t
                                            _ptr(s_w), _scale_fmt(s_w), _ptr(counts), E, int(max_m), _ptr(out),
                                            _out_code(out.dtype), _row_ld(out), N, K, _stream())
     check("fgb_batched_w8a8_block_gemm", st)
+    return out
+
+
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", select_bias: torch.Tensor | None = None,
+              renormalize: bool = True, scale: float = 1.0, out: tuple | None = None):
+    """The router of a mixture of experts: (ids int32 [T, top_k], weights float32 [T, top_k]).
+
+    logits bf16 or float32 [T, E] (unit inner stride).  The top_k largest of each row (ties: the lowest
+    index); with `select_bias` float32 [E] the largest of score + select_bias.  Weights are the scores
+    ("softmax" over the row or "sigmoid"), divided by the row's selected sum if `renormalize`, times
+    `scale`.  Experts at -inf (or NaN) are never selected: a row without top_k others ends in id -1 and
+    weight 0.  `out` = (ids, weights) writes into given contiguous buffers.
+    """
+    _need(isinstance(logits, torch.Tensor) and logits.dtype in _VALUES, "logits must be bf16 or float32")
+    _matrix(logits, "logits", logits.dtype)
+    T, E = logits.shape
+    score = _SCORES.get(scoring)
+    _need(score is not None, "scoring must be 'softmax' or 'sigmoid'")
+    _need(1 <= top_k <= E, f"top_k must be 1 .. {E}, got {top_k}")
+    if select_bias is not None:
+        _dense(select_bias, "select_bias", (torch.float32,), (E,))
+    if out is None:
+        _on_device(("logits", logits), ("select_bias", select_bias))
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        ids, weights = out
+        _dense(ids, "ids", (torch.int32,), (T, top_k))
+        _dense(weights, "weights", (torch.float32,), (T, top_k))
+        _on_device(("logits", logits), ("select_bias", select_bias), ("ids", ids), ("weights", weights))
+    st = lib().fgb_moe_route(_ptr(logits), _out_code(logits.dtype), _row_ld(logits), T, E, top_k, score,
+                             _ptr(select_bias), int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights),
+                             _stream())
+    check("fgb_moe_route", st)
+    return ids, weights
+
+
+def moe_ffn_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int) -> int:
+    return int(lib().fgb_moe_ffn_workspace_bytes(T, top_k, E, H, I))
+
+
+def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_q: torch.Tensor, s_w13: torch.Tensor,
+            w2_q: torch.Tensor, s_w2: torch.Tensor, activation: str = "silu", residual: torch.Tensor | None = None,
+            out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for a few tokens (T <= 64) on FP8 block weights:
+
+        y[t] = residual[t] + sum_j weights[t, j] * W2[e] . Q(act(W13[e, :I] . Q(x[t])) * (W13[e, I:] . Q(x[t])))
+
+    with e = ids[t, j] (ids outside 0 .. E-1 are skipped) and Q the 1x128-group E4M3 quantization
+    (scales within an ulp of quantize()'s).  x bf16 [T, H]; ids int32 and weights float32 [T, top_k] (moe_route's result); w13_q
+    uint8 [E, 2I, H] (gate rows, then up rows) and w2_q uint8 [E, H, I] with their 128x128 block scales
+    (float32 or UE8M0, both alike); activation "silu", "gelu" or "gelu_tanh"; residual bf16 or
+    float32 [T, H], which may be `out` itself.  `workspace`: moe_ffn_workspace_bytes(T, top_k, E, H, I)
+    bytes (allocated here when none is given).
+    """
+    _matrix(x, "x", torch.bfloat16)
+    T, H = x.shape
+    HB = _blocks(H, "H")
+    _need(T <= 64, "moe_ffn is for T <= 64 (use the grouped GEMM)")
+    _need(isinstance(w2_q, torch.Tensor) and w2_q.dim() == 3, "w2_q must be [E, H, I]")
+    E, _, I = w2_q.shape
+    IB = _blocks(I, "I")
+    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids must be [T, top_k]")
+    top_k = ids.shape[1]
+    _dense(ids, "ids", (torch.int32,), (T, top_k))
+    _dense(weights, "weights", (torch.float32,), (T, top_k))
+    _dense(w13_q, "w13_q", (torch.uint8,), (E, 2 * I, H))
+    _dense(w2_q, "w2_q", (torch.uint8,), (E, H, I))
+    _dense(s_w13, "s_w13", (torch.float32, torch.uint8), (E, 2 * IB, HB))
+    _dense(s_w2, "s_w2", (s_w13.dtype,), (E, HB, IB))
+    act = _ACTIVATIONS.get(activation)
+    _need(act in (ACT_SILU, ACT_GELU, ACT_GELU_TANH), "activation must be 'silu', 'gelu' or 'gelu_tanh'")
+    if residual is not None:
+        _need(isinstance(residual, torch.Tensor) and residual.dtype in _VALUES, "residual must be bf16 or float32")
+        _matrix(residual, "residual", residual.dtype, rows=T, cols=H)
+    if out is not None:
+        _need(isinstance(out, torch.Tensor) and out.dtype in _VALUES, "out must be bf16 or float32")
+        _matrix(out, "out", out.dtype, rows=T, cols=H)
+    if workspace is not None:
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
+    _on_device(("x", x), ("ids", ids), ("weights", weights), ("w13_q", w13_q), ("s_w13", s_w13), ("w2_q", w2_q),
+               ("s_w2", s_w2), ("residual", residual), ("out", out), ("workspace", workspace))
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    need = moe_ffn_workspace_bytes(T, top_k, E, H, I)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().fgb_moe_ffn(_ptr(x), _row_ld(x), _ptr(ids), _ptr(weights), top_k, _ptr(w13_q), _ptr(s_w13), _ptr(w2_q),
+                           _ptr(s_w2), _scale_fmt(s_w13), E, act, _ptr(residual),
+                           0 if residual is None else _out_code(residual.dtype),
+                           0 if residual is None else _row_ld(residual), _ptr(out), _out_code(out.dtype),
+                           _row_ld(out), T, H, I, _ptr(workspace), ws_bytes, _stream())
+    check("fgb_moe_ffn", st)
     return out
 
 

@@ -81,6 +81,9 @@ typedef enum {
   FGB_ACT_SILU = 4
 } fgb_activation;
 
+/* Score of fgb_moe_route. */
+typedef enum { FGB_SCORE_SOFTMAX = 0, FGB_SCORE_SIGMOID = 1 } fgb_score;
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* fgb_status_string(int status);
 
@@ -258,6 +261,57 @@ int fgb_batched_w8a8_block_gemm(const uint8_t* a_q, int64_t lda, const float* s_
  */
 int fgb_check_expert_offsets(const int32_t* expert_offsets, int32_t E, int64_t total_M, int32_t* result,
                              void* stream);
+
+/*
+ * Router of a mixture of experts: for every token the top_k experts of its row of logits, in
+ * descending order of the selection key, and their weights.
+ *   scores   FGB_SCORE_SOFTMAX: p = softmax over the row; FGB_SCORE_SIGMOID: p = 1 / (1 + exp(-l)).
+ *   keys     the logits (both scores grow with them), or p + select_bias with a selection bias, which
+ *            does not enter the weights; equal keys go to the lowest index.  (With a bias, keys that
+ *            differ by less than the float32 rounding of p + select_bias may come in either order.)
+ *   masking  an expert whose logit is -inf or NaN is never selected and has no share of the softmax;
+ *            a row with fewer than top_k open experts ends in ids -1 with weight 0.
+ *   weights  p, or with renormalize != 0 p / (sum of the row's selected p), times `scale`.
+ *   logits   [T, ld] bf16 or float32 per logits_dtype (fgb_out_dtype values), ld >= E, aligned to the
+ *            element; select_bias float32 [E] or NULL; ids int32 and weights float32 [T, top_k] dense,
+ *            4-byte aligned.  1 <= E <= 1024, 1 <= top_k <= min(E, 32); T == 0 is a no-op.
+ * ids and weights are what fgb_moe_ffn takes.  One launch, no workspace.
+ */
+int fgb_moe_route(const void* logits, int logits_dtype, int64_t ld, int64_t T, int32_t E, int32_t top_k,
+                  int scoring, const float* select_bias, int renormalize, float scale,
+                  int32_t* ids, float* weights, void* stream);
+
+/* Host query: workspace bytes fgb_moe_ffn needs (0 for shapes it rejects). */
+size_t fgb_moe_ffn_workspace_bytes(int64_t T, int32_t top_k, int32_t E, int64_t H, int64_t I);
+
+/*
+ * A whole mixture-of-experts layer on fine-grained FP8 weights for a few tokens (the expert matmuls of
+ * Transformers "Fine-grained FP8", "DeepGEMM fast path"), from bf16 rows to finished rows:
+ *   y[t] = residual[t] + sum_j weights[t, j] * W2[e] . Q(act(W13[e][0:I] . Q(x[t])) * (W13[e][I:2I] . Q(x[t])))
+ * with e = ids[t, j] and Q the 1x128-group quantization: s = fl32(amax * fl32(1 / 448)), an ulp at most
+ * from fgb_act_quant_group128's fl32(amax / 448), codes E4M3(fl32(v / s)), of x and of the float32 gated
+ * product.  Sums, the activation, the gate and the combination are float32; y is rounded once.
+ *   x         bf16 [T, ldx], 16-byte aligned rows, ldx >= H;
+ *   ids       int32 [T, top_k]; an id outside 0 .. E-1 is skipped (an expert that lives elsewhere); an
+ *             expert named twice by one token counts once, with the sum of its weights;
+ *   weights   float32 [T, top_k];
+ *   w13_q     E4M3 [E, 2I, H] (gate rows, then up rows), s_w13 [E, 2I/128, H/128];
+ *   w2_q      E4M3 [E, H, I], s_w2 [E, H/128, I/128]; scales float32 or UE8M0 per s_w_fmt;
+ *   activation  FGB_ACT_SILU, FGB_ACT_GELU or FGB_ACT_GELU_TANH (FGB_ERR_ENUM otherwise);
+ *   residual  [T, ldr] bf16 or float32 per residual_dtype, 16-byte aligned rows, or NULL; may be y
+ *             itself (same type and pitch);
+ *   y         [T, ldy] bf16 or float32 per y_dtype, 16-byte aligned rows;
+ *   workspace device, 16-byte aligned, >= fgb_moe_ffn_workspace_bytes(T, top_k, E, H, I) bytes,
+ *             contents ignored on entry.
+ * 0 <= T <= 64 (more tokens: fgb_grouped_w8a8_block_gemm), T * top_k <= 1024, 1 <= E <= 1024, H and I
+ * multiples of 128 up to 32768 (FGB_ERR_SHAPE otherwise).  Only routed experts' weights
+ * are read; results do not depend on the order of execution.
+ */
+int fgb_moe_ffn(const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int32_t top_k,
+                const uint8_t* w13_q, const void* s_w13, const uint8_t* w2_q, const void* s_w2, int s_w_fmt,
+                int32_t E, int activation, const void* residual, int residual_dtype, int64_t ldr,
+                void* y, int y_dtype, int64_t ldy, int64_t T, int64_t H, int64_t I,
+                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The other FP8 schemes.  FP8_DYNAMIC (vLLM "FP8 W8A8", "Quantization process": static
