@@ -6,21 +6,24 @@
 //
 // What bounds it: every routed expert's 3 H I weight bytes are read once, and a token's share of
 // arithmetic on them is small, so the layer runs at the rate of the weight stream (HBM).  Three
-// launches:
-//   prep    sorts the (token, expert) pairs by expert into 16-row tiles and quantizes each pair's row
-//           of x into its tile;
+// launches, two for the fewest tokens:
+//   prep    quantizes the rows of x and, in one more workgroup, sorts the (token, expert) pairs by
+//           expert into tiles of 16 rows;
 //   gate+up a workgroup owns 128 columns of the intermediate of one expert: 8 waves, each streaming
 //           its 16 gate rows and 16 up rows over the whole H against the expert's tiles (one
 //           activation fragment serves both), so that act(gate) * up and its group's maximum stay in
-//           the workgroup and the codes of the quantized product are all that is written;
-//   down    a workgroup owns 32 columns of y: its 8 waves split the routed experts' K-blocks, add
+//           the workgroup and the codes of the quantized product are all that is written.  With the
+//           fewest tokens each workgroup finds its expert and quantizes its rows itself, and there is
+//           no prep launch;
+//   down    a workgroup owns 16 or 32 columns of y: its waves split the routed experts' K-blocks, add
 //           their weighted contributions per token in LDS in a fixed order, and the workgroup adds
-//           the waves' sums and the residual.  No partial sums in memory, no atomics.
-// Codes lie in the workspace in the matrix instruction's operand order: tile, K-block, 16-byte half,
-// lane (16 g + r holds bytes 32 g .. 32 g + 31 of row r), so a fragment is two loads of whole lines
-// however the rows were gathered.  Rows of a tile past its count are neither written nor read.
-// Weights are loaded as whole lines and reordered through a per-wave LDS tile (as in the decode GEMM's
-// register kernel), D K-blocks in flight per wave.
+//           the waves' sums and the residual.  No partial sums in memory; the only atomics are the
+//           integer counters of the sort, whose order moves rows within a tile and changes no value.
+// The gated product's codes lie in the workspace in the matrix instruction's operand order: tile,
+// K-block, 16-byte half, lane (16 g + r holds bytes 32 g .. 32 g + 31 of row r), so a fragment is two
+// loads of whole lines.  Rows of a tile past its count are neither written nor read.  Weights are
+// loaded as whole lines and reordered through a per-wave LDS tile (as in the decode GEMM's register
+// kernel), several K-blocks in flight per wave.
 #include <type_traits>
 
 #include "epilogue.hpp"
@@ -49,9 +52,9 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return cvt_pk_e4m3<true>(c / v, d / v, cvt_pk_e4m3<false>(a / v, b / v, 0u));
 }
 
-// Workspace: the routed experts in ascending order, each with its first tile and its row count; the
-// tiles' rows (token and weight); the codes and scales of x and of the gated product.  Scales are
-// [tile][K-block][16 rows].
+// Workspace: the routed experts, each with its first tile and its row count; the tiles' rows (token
+// and weight); codes [T, H] and scales [T, H/128] of x; the gated product's codes and scales, the
+// scales [tile][K-block][16 rows].
 struct Space {
   int* active;         // number of routed experts
   int4* experts;       // {expert, first tile, rows, 0}
@@ -80,8 +83,8 @@ size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
   t.experts = (int4*)take(max_experts(T, top_k, E) * sizeof(int4));
   t.row_token = (int*)take(rows * sizeof(int));
   t.row_weight = (float*)take(rows * sizeof(float));
-  t.xq = take(rows * H);
-  t.xs = (float*)take(rows * (H / 128) * sizeof(float));
+  t.xq = take((size_t)T * H);
+  t.xs = (float*)take((size_t)T * (H / 128) * sizeof(float));
   t.hq = take(rows * I);
   t.hs = (float*)take(rows * (I / 128) * sizeof(float));
   if (s) *s = t;
@@ -89,134 +92,79 @@ size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// prep: one workgroup per (token, choice) pair.  Every workgroup counts the pairs per expert (at most
-// 1024 of each) and finds its own pair's tile and row: the tiles of the experts before its own,
-// then its rank among the expert's pairs in pair order.  A pair whose expert its token has named
-// already is dropped and its weight goes to the first (so a token has one row per expert).
-// Workgroup 0 also writes the table of routed experts.
+// prep: workgroups 0 .. T-1 quantize a row of x each, workgroup T sorts the pairs: counts per expert
+// (an LDS counter hands a pair its rank), an exclusive scan over the experts places the routed ones
+// and their tiles.  A pair whose expert its token has named already is dropped and its weight goes
+// to the first, so a token has one row per expert.
 // ---------------------------------------------------------------------------------------------
-constexpr int PREP = 256;
+constexpr int PREP = 1024;  // pairs and experts at most: one each per thread
+static_assert(kMoeMaxPairs <= PREP && kMoeMaxExperts <= PREP, "one pair and one expert per thread");
+
+// Codes of 16 consecutive values of row x (chunk c) and, from the chunk's first lane, the group's
+// scale.  8 lanes share a group; whole groups are active.
+__device__ __forceinline__ int4 quant_chunk(const uint16_t* x, int c, float& sc) {
+  const int4 a = gload_i4(x + 16 * c), b = gload_i4(x + 16 * c + 8);
+  const uint4 u = make_uint4(a.x, a.y, a.z, a.w), v = make_uint4(b.x, b.y, b.z, b.w);
+  sc = row8_max(fmaxf(absmax8(u), absmax8(v))) * kInvMax;
+  int4 q;
+  q.x = codes4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y), sc);
+  q.y = codes4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w), sc);
+  q.z = codes4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), sc);
+  q.w = codes4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), sc);
+  return q;
+}
 
 __global__ __launch_bounds__(PREP) void moe_prep_kernel(MoeArgs p, Space s) {
   __shared__ int sid[kMoeMaxPairs];
   __shared__ int cnt[kMoeMaxExperts];
-  __shared__ int part[3][PREP / 64];
+  __shared__ int first_tile[kMoeMaxExperts];
+  __shared__ int part[PREP / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int pair = blockIdx.x, P = p.T * p.top_k;
-  for (int e = tid; e < p.E; e += PREP) cnt[e] = 0;
-  for (int q = tid; q < P; q += PREP) sid[q] = gload<int>(p.ids + q);
-  __syncthreads();
-  // drop foreign ids and repeats (a repeat looks at the ids as they came: dropping is decided from
-  // registers before any is overwritten)
-  int kept[kMoeMaxPairs / PREP];
-#pragma unroll
-  for (int i = 0; i < kMoeMaxPairs / PREP; ++i) {
-    const int q = tid + i * PREP;
-    kept[i] = -1;
-    if (q < P) {
-      const int id = sid[q];
-      bool keep = id >= 0 && id < p.E;
-      for (int f = q / p.top_k * p.top_k; f < q; ++f) keep = keep && sid[f] != id;
-      kept[i] = keep ? id : -1;
+  if ((int)blockIdx.x < p.T) {
+    const int t = blockIdx.x;
+    for (int c = tid; c < p.H / 16; c += PREP) {
+      float sc;
+      const int4 q = quant_chunk(p.x + (int64_t)t * p.ldx, c, sc);
+      gstore<v4i>(s.xq + (int64_t)t * p.H + 16 * c, v4i{q.x, q.y, q.z, q.w});
+      if (c % 8 == 0) gstore<float>(s.xs + (int64_t)t * (p.H / 128) + c / 8, sc);
     }
+    return;
   }
-  const int first = pair / p.top_k * p.top_k;
-  const int raw = sid[pair];
-  float weight = 0.0f;
-  if (tid == 0) {
-    for (int f = pair; f < first + p.top_k; ++f)
-      if (sid[f] == raw) weight += gload<float>(p.weights + f);
-  }
+  const int P = p.T * p.top_k;
+  const int id = tid < P ? gload<int>(p.ids + tid) : -1;
+  const float w = tid < P ? gload<float>(p.weights + tid) : 0.0f;
+  sid[tid] = id;
+  cnt[tid] = 0;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kMoeMaxPairs / PREP; ++i) {
-    const int q = tid + i * PREP;
-    if (q < P) {
-      sid[q] = kept[i];
-      if (kept[i] >= 0) atomicAdd(&cnt[kept[i]], 1);
-    }
-  }
+  const int first = tid / p.top_k * p.top_k;
+  bool keep = id >= 0 && id < p.E;
+  for (int q = first; q < tid; ++q) keep = keep && sid[q] != id;
+  const int rank = keep ? atomicAdd(&cnt[id], 1) : 0;
   __syncthreads();
-  const int id = sid[pair];
-  // rank of this pair among its expert's, tiles and routed experts before its expert
-  int rank = 0, tiles = 0;
-  for (int q = tid; q < pair; q += PREP) rank += sid[q] == id;
-  for (int e = tid; e < id; e += PREP) tiles += (cnt[e] + kTile - 1) / kTile;
+  // expert tid: routed or not, its tiles; both scanned in one integer (at most 1024 and 1088)
+  const int rows = cnt[tid];
+  const int both = (rows > 0) + ((rows + kTile - 1) / kTile << 16);
+  int inc = both;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    rank += __shfl_xor(rank, d);
-    tiles += __shfl_xor(tiles, d);
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
   }
-  if (lane == 0) {
-    part[0][wave] = rank;
-    part[1][wave] = tiles;
-  }
-  if (pair == 0) {
-    // the table: thread i owns experts 4 i .. 4 i + 3; an exclusive scan of (routed, tiles) over the
-    // threads places them
-    int c[kMoeMaxExperts / PREP], na = 0, nt = 0;
-#pragma unroll
-    for (int i = 0; i < kMoeMaxExperts / PREP; ++i) {
-      const int e = tid * (kMoeMaxExperts / PREP) + i;
-      c[i] = e < p.E ? cnt[e] : 0;
-      na += c[i] > 0;
-      nt += (c[i] + kTile - 1) / kTile;
-    }
-    int both = na + (nt << 16), inc = both;  // (at most 1024 and 1088)
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(inc, d);
-      if (lane >= d) inc += o;
-    }
-    if (lane == 63) part[2][wave] = inc;
-    __syncthreads();
-    int before = inc - both;
-    for (int w = 0; w < wave; ++w) before += part[2][w];
-    int a = before & 0xFFFF, t = before >> 16;
-#pragma unroll
-    for (int i = 0; i < kMoeMaxExperts / PREP; ++i) {
-      if (c[i] > 0) {
-        s.experts[a] = make_int4(tid * (kMoeMaxExperts / PREP) + i, t, c[i], 0);
-        ++a;
-        t += (c[i] + kTile - 1) / kTile;
-      }
-    }
-    if (tid == PREP - 1) *s.active = a;
-  } else {
-    __syncthreads();
-  }
-  if (id < 0) return;
-  rank = tiles = 0;
-#pragma unroll
-  for (int w = 0; w < PREP / 64; ++w) {
-    rank += part[0][w];
-    tiles += part[1][w];
-  }
-  const int tile = tiles + rank / kTile, row = rank % kTile;
-  if (tid == 0) {
-    s.row_token[tile * kTile + row] = pair / p.top_k;
-    s.row_weight[tile * kTile + row] = weight;
-  }
-  // the row's codes: 16 lanes per 128-group, 8 values per lane, as the activation quantizer does
-  const int KB = p.H / 128;
-  const uint16_t* x = p.x + (int64_t)(pair / p.top_k) * p.ldx;
-  uint8_t* xq = s.xq + (int64_t)tile * KB * kFrag;
-  // (whole waves for the row maxima: lanes past the row repeat its first group and store nothing)
-  for (int c0 = wave * 64; c0 < p.H / 8; c0 += PREP) {
-    const bool in = c0 + lane < p.H / 8;
-    const int c = in ? c0 + lane : lane % 16;
-    const int4 v = gload_i4(x + 8 * c);
-    const uint4 u = make_uint4(v.x, v.y, v.z, v.w);
-    const float sc = row16_max(absmax8(u)) * kInvMax;
-    const float v8[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
-                         bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
-    if (!in) continue;
-    const int kb = c / 16, k = c % 16 * 8;
-    v2u w;
-    w[0] = codes4(v8[0], v8[1], v8[2], v8[3], sc);
-    w[1] = codes4(v8[4], v8[5], v8[6], v8[7], sc);
-    gstore<v2u>(xq + kb * kFrag + (k % 32) / 16 * 1024 + (k / 32 * 16 + row) * 16 + k % 16, w);
-    if (c % 16 == 0) gstore<float>(s.xs + ((int64_t)tile * KB + kb) * kTile + row, sc);
+  if (lane == 63) part[wave] = inc;
+  __syncthreads();
+  for (int q = 0; q < wave; ++q) inc += part[q];
+  const int at = (inc - both) & 0xFFFF, tile = (inc - both) >> 16;
+  first_tile[tid] = tile;
+  if (rows > 0) s.experts[at] = make_int4(tid, tile, rows, 0);
+  if (tid == PREP - 1) *s.active = inc & 0xFFFF;
+  __syncthreads();
+  if (keep) {
+    float sum = w;  // with the weights of later pairs that name the same expert
+    for (int q = tid + 1; q < first + p.top_k; ++q)
+      if (sid[q] == id) sum += gload<float>(p.weights + q);
+    const int row = first_tile[id] * kTile + rank;
+    s.row_token[row] = tid / p.top_k;
+    s.row_weight[row] = sum;
   }
 }
 
@@ -254,27 +202,17 @@ __device__ __forceinline__ v4f block_sum(const Wide& a, const Wide& b) {
   return s;
 }
 
-struct Codes {
+__device__ __forceinline__ v8i codes8(const int4& lo, const int4& hi) {
   v8i v;
-};
-__device__ __forceinline__ Codes narrow(const int4& lo, const int4& hi) {
-  Codes c;
-  c.v[0] = lo.x; c.v[1] = lo.y; c.v[2] = lo.z; c.v[3] = lo.w;
-  c.v[4] = hi.x; c.v[5] = hi.y; c.v[6] = hi.z; c.v[7] = hi.w;
-  return c;
-}
-__device__ __forceinline__ v4f block_sum(const Codes& a, const Codes& b) { return mfma_e4m3_16x16x128(a.v, b.v); }
-
-template <bool WIDE>
-__device__ __forceinline__ auto operand(const int4& lo, const int4& hi) {
-  if constexpr (WIDE) return widen(lo, hi);
-  else return narrow(lo, hi);
+  v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+  v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  return v;
 }
 
 // ---------------------------------------------------------------------------------------------
 // One wave's stream: NT weight tiles (16 rows each) against MT activation tiles over nk K-blocks,
 // D blocks in flight in registers.
-//   acc[n][m] += P * (s_a * s_w[n])   per K-block, P the block's product sums (WIDE: from bf16).
+//   acc[n][m] += P * (s_a * s_w[n])   per K-block, P the block's product sums.
 // w[n]: lane address of weight tile n at the first block (row l/8, 16-byte chunk l%8), rows 8 further
 // at + 8 * pitch; a[m]: lane address of tile m's fragment; sa[m]: lane address of its row's scale;
 // `scale(n, kk)` gives the weight block's scale.  Lanes whose row does not exist are given the
@@ -282,7 +220,7 @@ __device__ __forceinline__ auto operand(const int4& lo, const int4& hi) {
 // Blocks past the end are clamped to the last one, so the loads in flight are the same number in
 // every step.
 // ---------------------------------------------------------------------------------------------
-template <int NT, int MT, int D, bool WIDE, typename Scale>
+template <int NT, int MT, int D, typename Scale>
 __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int64_t pitch, const uint8_t* const (&a)[MT],
                                               const float* const (&sa)[MT], int nk, uint8_t* lds,
                                               Scale scale, v4f (&acc)[NT][MT]) {
@@ -314,28 +252,33 @@ __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int
       *reinterpret_cast<int4*>(t + wo0) = wv[d][n][0];
       *reinterpret_cast<int4*>(t + wo1) = wv[d][n][1];
     }
-    decltype(operand<WIDE>(av[d][0][0], av[d][0][1])) af[MT];
+    v8i af[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) af[m] = operand<WIDE>(av[d][m][0], av[d][m][1]);
+    for (int m = 0; m < MT; ++m) af[m] = codes8(av[d][m][0], av[d][m][1]);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint8_t* t = lds + n * kFrag;
-      const int4 lo = *reinterpret_cast<const int4*>(t + ro0);
-      const int4 hi = *reinterpret_cast<const int4*>(t + ro1);
-      const auto wf = operand<WIDE>(lo, hi);
+      const v8i wf = codes8(*reinterpret_cast<const int4*>(t + ro0), *reinterpret_cast<const int4*>(t + ro1));
       const float sw = scale(n, kk);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[n][m] += block_sum(wf, af[m]) * (sv[d][m] * sw);
+      for (int m = 0; m < MT; ++m) {
+        acc[n][m] += mfma_e4m3_16x16x128(wf, af[m]) * (sv[d][m] * sw);
+        asm volatile("" : "+v"(acc[n][m]));
+      }
     }
   };
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) load(min(d, nk - 1), d);
+  __builtin_amdgcn_sched_barrier(0);
   int kk = 0;
   for (; kk + D <= nk; kk += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
+      // (pinned: left to itself the scheduler sinks the loads to just before their use)
       load(min(kk + d + D - 1, nk - 1), (d + D - 1) % D);
+      __builtin_amdgcn_sched_barrier(0);
       compute(kk + d, d);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
@@ -343,14 +286,57 @@ __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int
     if (kk + d < nk) compute(kk + d, d);
 }
 
+// 16 bytes at base + lane_off + off: buffer form, scalar base and scalar offset, so that a stream of
+// loads holds one address register per row.  AUX: kLastReadAux for weights (read for the last time).
+template <int AUX>
+__device__ __forceinline__ int4 bload16(const void* base, uint32_t lane_off, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the builtins exist in the device pass only)
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00020000);
+  const v4i v = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, lane_off, off, AUX));
+  return make_int4(v[0], v[1], v[2], v[3]);
+#else
+  return make_int4(0, 0, 0, 0);
+#endif
+}
+__device__ __forceinline__ float bload4(const void* base, uint32_t lane_off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00020000);
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, lane_off, 0, 0));
+#else
+  return 0.0f;
+#endif
+}
+
+// Barrier after LDS writes that other waves read next, without the fence that would also wait for
+// every weight load in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));  // lgkmcnt(0), vmcnt and expcnt at their maxima
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------------------------
 // gate+up: grid (I / 128, routed experts at most), 8 waves.
+//
+// The expert's activation codes go through LDS, once for the 8 waves: chunks of CH K-blocks, two
+// buffers, the next chunk loaded into registers while the current one is multiplied.  (Loaded by each
+// wave into registers, the activations of a popular expert's 64 rows were 2 x 4 KB per 4 KB of
+// weights, and as vector-memory loads complete in order, waiting for them waited for the weight
+// loads issued before them.)  In LDS, 16-byte chunk c of row r of K-block k sits at slot r ^ (c + 8 (k & 1))
+// of its 16-slot group: writes of one row's 16 chunks and reads of one chunk of 16 rows both hit 16
+// distinct bank groups.
+// MTMAX: the most 16-row tiles an expert can have (T <= 16 MTMAX).
 // ---------------------------------------------------------------------------------------------
-template <int SWF>
-__global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeArgs p, Space s) {
-  __shared__ __attribute__((aligned(1024))) uint8_t tiles[8][2 * kFrag];
-  __shared__ float sws[2][256];      // the two weight block rows' scales (H <= 32768)
-  __shared__ float amax[8][4 * kTile];
+constexpr int CH = 4;  // K-blocks per chunk and weight blocks in registers per wave
+
+template <int SWF, int MTMAX>
+__global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s) {
+  __shared__ __attribute__((aligned(1024))) uint8_t wtiles[8][2 * kFrag];
+  __shared__ __attribute__((aligned(1024))) uint8_t atiles[2][CH * MTMAX * kFrag];
+  __shared__ float ascale[2][CH][MTMAX * kTile];
+  __shared__ float sws[2][256];  // the two weight block rows' scales (H <= 32768)
+  __shared__ float amax[8][MTMAX * kTile];
   if ((int)blockIdx.y >= gload<int>(s.active)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -359,33 +345,118 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeArgs p, Space s) {
   const int e = __builtin_amdgcn_readfirstlane(ex[0]), tile0 = __builtin_amdgcn_readfirstlane(ex[1]);
   const int rows = __builtin_amdgcn_readfirstlane(ex[2]);
   const int KB = p.H / 128, NB = p.I / 128, gb = blockIdx.x;
-  const int64_t sw0 = ((int64_t)e * 2 * NB + gb) * KB;
-  for (int k = tid; k < KB; k += 512) {
-    sws[0][k] = load_sw<SWF>(p.s_w13, sw0 + k);
-    sws[1][k] = load_sw<SWF>(p.s_w13, sw0 + (int64_t)NB * KB + k);
-  }
-  __syncthreads();
-  const uint8_t* w0 = p.w13_q + ((int64_t)e * 2 * p.I + gb * 128 + wave * 16 + (lane >> 3)) * p.H + 16 * (lane & 7);
-  const uint8_t* const w[2] = {w0, w0 + (int64_t)p.I * p.H};
+  // this lane's weight bytes from the expert's first: 32-bit offsets (2 I H <= 2^31), the K-block is the
+  // buffer load's scalar offset
+  const uint32_t wrow = (uint32_t)((gb * 128 + wave * 16 + (lane >> 3)) * p.H + 16 * (lane & 7));
+  const uint32_t up = (uint32_t)p.I * p.H, pitch8 = 8u * p.H;
+  const uint32_t woff[4] = {wrow, wrow + pitch8, wrow + up, wrow + up + pitch8};
+  const uint8_t* const wexp = p.w13_q + (int64_t)e * 2 * p.I * p.H;
+  const int wo0 = swz(lane >> 3, lane & 7), wo1 = swz((lane >> 3) + 8, lane & 7);
+  const int ro0 = swz(r, 2 * g), ro1 = swz(r, 2 * g + 1);
+  uint8_t* const wt = &wtiles[wave][0];
 
   auto run = [&](auto mt_c) {
     constexpr int MT = decltype(mt_c)::value;
-    constexpr int D = MT >= 4 ? 2 : 3;
-    const uint8_t* a[MT];
-    const float* sa[MT];
+    // weights: blocks past the end repeat the last one (their scale is 0)
+    int4 wv[CH][2][2];
+    auto load = [&](int kk, int d) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int q = min(m * kTile + r, rows - 1);  // (MT = 4 may run three tiles)
-      a[m] = s.xq + (int64_t)(tile0 + q / kTile) * KB * kFrag + (g * kTile + q % kTile) * 16;
-      sa[m] = s.xs + (int64_t)(tile0 + q / kTile) * KB * kTile + q % kTile;
-    }
+      for (int i = 0; i < 4; ++i) wv[d][i / 2][i % 2] = bload16<kLastReadAux>(wexp, woff[i], (uint32_t)min(kk, KB - 1) * 128);
+    };
+    // activations: a chunk is CH * 128 contiguous bytes of each row; copy i of a thread takes 16 of them
+    // (rows past the count repeat the last one)
+    constexpr int RC = CH * 8, NA = MT * kTile * RC / 512, RPC = 512 / RC;  // 16-byte pieces per row, copies, rows per copy
+    static_assert(NA * 512 == MT * kTile * RC && kTile % RPC == 0, "whole copies");
+    int4 av[NA];
+    float sv = 0.0f;
+    const int ak = tid % RC / 8, ac = tid & 7, ar = tid / RC;
+    uint32_t aoff[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      aoff[i] = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(i * RPC + ar, rows - 1)) * p.H + 16 * ac;
+    const int sk = tid / (MT * kTile), sr = tid % (MT * kTile);  // scale of row sr, block sk < CH
+    const uint32_t soff = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(sr, rows - 1)) * KB * 4;
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) av[i] = bload16<0>(s.xq, aoff[i] + min(k0 + ak, KB - 1) * 128, 0);
+      sv = bload4(s.xs, soff + min(k0 + min(sk, CH - 1), KB - 1) * 4);
+    };
+    auto stash = [&](int k0, int buf) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const int q = i * RPC + ar;
+        *reinterpret_cast<int4*>(&atiles[buf][(ak * MT + q / kTile) * kFrag + (ac & 1) * 1024 +
+                                              ((ac >> 1) * 16 + ((q % kTile) ^ (ac + 8 * (ak & 1)))) * 16]) = av[i];
+      }
+      if (sk < CH) ascale[buf][sk][sr] = k0 + sk < KB ? sv : 0.0f;
+    };
     v4f acc[2][MT];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[n][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_blocks<2, MT, D, true>(w, p.H, a, sa, KB, &tiles[wave][0],
-                            [&](int n, int kk) { return sws[n][kk]; }, acc);
+    auto compute = [&](int kk, int d, int buf) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        // (a wave's LDS operations complete in order: the reads see the writes, and the next block's
+        // writes follow these reads)
+        *reinterpret_cast<int4*>(wt + n * kFrag + wo0) = wv[d][n][0];
+        *reinterpret_cast<int4*>(wt + n * kFrag + wo1) = wv[d][n][1];
+      }
+      Wide wf[2];
+      float sw[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        wf[n] = widen(*reinterpret_cast<const int4*>(wt + n * kFrag + ro0), *reinterpret_cast<const int4*>(wt + n * kFrag + ro1));
+        sw[n] = sws[n][min(kk, KB - 1)];
+      }
+      const uint8_t* t = &atiles[buf][d * MT * kFrag];
+      const int lo = (g * 16 + (r ^ (2 * g + 8 * (d & 1)))) * 16, hi = 1024 + (g * 16 + (r ^ (2 * g + 1 + 8 * (d & 1)))) * 16;
+      int4 alo = *reinterpret_cast<const int4*>(t + lo), ahi = *reinterpret_cast<const int4*>(t + hi);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const Wide af = widen(alo, ahi);
+        const float sa = ascale[buf][d][m * kTile + r];
+        if (m + 1 < MT) {
+          alo = *reinterpret_cast<const int4*>(t + (m + 1) * kFrag + lo);
+          ahi = *reinterpret_cast<const int4*>(t + (m + 1) * kFrag + hi);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          acc[n][m] += block_sum(wf[n], af) * (sa * sw[n]);
+          // (the sum is due here: left alone, the compiler keeps every block's product sums to the end
+          // of the chunk, in the registers that the weights in flight need)
+          asm volatile("" : "+v"(acc[n][m]));
+        }
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < CH - 1; ++d) load(d, d);
+    fetch(0);
+    __builtin_amdgcn_sched_barrier(0);
+    const int64_t sw0 = ((int64_t)e * 2 * NB + gb) * KB;
+    for (int k = tid; k < KB; k += 512) {
+      sws[0][k] = load_sw<SWF>(p.s_w13, sw0 + k);
+      sws[1][k] = load_sw<SWF>(p.s_w13, sw0 + (int64_t)NB * KB + k);
+    }
+    stash(0, 0);
+    lds_barrier();
+    int buf = 0;
+    for (int k0 = 0; k0 < KB; k0 += CH) {
+      fetch(k0 + CH);  // (past the end: the last block again, stashed where nothing reads it)
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int d = 0; d < CH; ++d) {
+        // (pinned: left to itself the scheduler sinks the loads to just before their use)
+        load(k0 + d + CH - 1, (d + CH - 1) % CH);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(k0 + d, d, buf);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      stash(k0 + CH, buf ^ 1);
+      lds_barrier();
+      buf ^= 1;
+    }
     // the gated product of this wave's 16 columns (lane: row r, columns 4 g .. 4 g + 3) and the rows'
     // maxima over the workgroup's 128 columns
     v4f h[MT];
@@ -418,30 +489,30 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeArgs p, Space s) {
       }
     }
   };
-  // (an expert has at most T <= 64 rows: four tiles)
-  if (rows <= 16) run(std::integral_constant<int, 1>{});
-  else if (rows <= 32) run(std::integral_constant<int, 2>{});
-  else run(std::integral_constant<int, 4>{});
+  if (MTMAX == 1 || rows <= 16) run(std::integral_constant<int, 1>{});
+  else if (MTMAX == 2 || rows <= 32) run(std::integral_constant<int, MTMAX < 2 ? 1 : 2>{});
+  else run(std::integral_constant<int, MTMAX < 4 ? 1 : 4>{});
 }
 
 // ---------------------------------------------------------------------------------------------
-// down: grid H / 32, 8 waves.  The K-blocks of all routed experts, in expert order, are one list that
-// the waves split evenly; a wave walks its share expert by expert (segments).
+// down: grid H / (16 NT), WK waves.  The K-blocks of all routed experts, in expert order, are one list
+// that the waves split evenly; a wave walks its share expert by expert (segments).
 // ---------------------------------------------------------------------------------------------
-template <int SWF, int OUT>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs p, Space s) {
-  __shared__ __attribute__((aligned(1024))) uint8_t tiles[8][2 * kFrag];
-  extern __shared__ __attribute__((aligned(16))) float ysum[];  // [8 waves][T][32]
+template <int SWF, int OUT, int MTMAX, int NT, int WK>
+__global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
+  constexpr int COLS = 16 * NT;
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[WK][NT * kFrag];
+  extern __shared__ __attribute__((aligned(16))) float ysum[];  // [WK waves][T][COLS]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 32;
+  const int n0 = blockIdx.x * COLS;
   const int KB = p.I / 128, NB = p.H / 128;
-  float* const mine = ysum + wave * p.T * 32;
-  for (int i = lane; i < p.T * 8; i += 64) *reinterpret_cast<v4f*>(mine + 4 * i) = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  float* const mine = ysum + wave * p.T * COLS;
+  for (int i = lane; i < p.T * (COLS / 4); i += 64) *reinterpret_cast<v4f*>(mine + 4 * i) = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   const int units = gload<int>(s.active) * KB;
-  const int per = (units + 7) / 8;
+  const int per = (units + WK - 1) / WK;
   int u = __builtin_amdgcn_readfirstlane(min(units, wave * per));
   const int u1 = __builtin_amdgcn_readfirstlane(min(units, (wave + 1) * per));
   while (u < u1) {
@@ -452,10 +523,12 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs p, Space s) {
     const int rows = __builtin_amdgcn_readfirstlane(ex[2]);
     const float swl = lane < nk ? load_sw<SWF>(p.s_w2, ((int64_t)e * NB + n0 / 128) * KB + kb0 + lane) : 0.0f;
     const uint8_t* w0 = p.w2_q + ((int64_t)e * p.H + n0 + (lane >> 3)) * p.I + (int64_t)kb0 * 128 + 16 * (lane & 7);
-    const uint8_t* const w[2] = {w0, w0 + (int64_t)16 * p.I};
+    const uint8_t* w[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) w[n] = w0 + (int64_t)16 * n * p.I;
     auto run = [&](auto mt_c) {
       constexpr int MT = decltype(mt_c)::value;
-      constexpr int D = MT >= 4 ? 2 : 3;
+      constexpr int D = 3;  // blocks in registers (4: 2-8% slower with one row tile, registers; 2: 5% with four)
       const uint8_t* a[MT];
       const float* sa[MT];
 #pragma unroll
@@ -464,12 +537,12 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs p, Space s) {
         a[m] = s.hq + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kFrag + (g * kTile + q % kTile) * 16;
         sa[m] = s.hs + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kTile + q % kTile;
       }
-      v4f acc[2][MT];
+      v4f acc[NT][MT];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[n][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      stream_blocks<2, MT, D, false>(w, p.I, a, sa, nk, &tiles[wave][0],
+      stream_blocks<NT, MT, D>(w, p.I, a, sa, nk, &tiles[wave][0],
                               [&](int, int kk) {
                                 return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), kk));
                               }, acc);
@@ -481,25 +554,25 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs p, Space s) {
           const int t = gload<int>(s.row_token + row);
           const float wt = gload<float>(s.row_weight + row);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            v4f* const q = reinterpret_cast<v4f*>(mine + t * 32 + n * 16 + 4 * g);
+          for (int n = 0; n < NT; ++n) {
+            v4f* const q = reinterpret_cast<v4f*>(mine + t * COLS + n * 16 + 4 * g);
             *q += acc[n][m] * wt;
           }
         }
       }
     };
-    if (rows <= 16) run(std::integral_constant<int, 1>{});
-    else if (rows <= 32) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 4>{});
+    if (MTMAX == 1 || rows <= 16) run(std::integral_constant<int, 1>{});
+    else if (MTMAX == 2 || rows <= 32) run(std::integral_constant<int, MTMAX < 2 ? 1 : 2>{});
+    else run(std::integral_constant<int, MTMAX < 4 ? 1 : 4>{});
     u += nk;
   }
   __syncthreads();
   // the waves' sums in wave order, the residual, one rounding
-  for (int i = tid; i < p.T * 8; i += 512) {
-    const int t = i >> 3, c = (i & 7) * 4;
-    v4f sum = *reinterpret_cast<const v4f*>(ysum + t * 32 + c);
+  for (int i = tid; i < p.T * (COLS / 4); i += 64 * WK) {
+    const int t = i / (COLS / 4), c = i % (COLS / 4) * 4;
+    v4f sum = *reinterpret_cast<const v4f*>(ysum + t * COLS + c);
 #pragma unroll
-    for (int q = 1; q < 8; ++q) sum += *reinterpret_cast<const v4f*>(ysum + (q * p.T + t) * 32 + c);
+    for (int q = 1; q < WK; ++q) sum += *reinterpret_cast<const v4f*>(ysum + (q * p.T + t) * COLS + c);
     if (p.residual != nullptr) {
       float f[4];
       load_values<4>(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n0 + c, f);
@@ -515,26 +588,50 @@ size_t moe_ffn_workspace_bytes(int T, int top_k, int E, int H, int I) {
   return layout(T, top_k, E, H, I, nullptr, nullptr);
 }
 
+namespace {
+
+template <int MTMAX>
+hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
+  hipLaunchKernelGGL(moe_prep_kernel, dim3((unsigned)a.T + 1), dim3(PREP), 0, stream, a, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 up((unsigned)(a.I / 128), (unsigned)max_experts(a.T, a.top_k, a.E));
+  if (a.s_w_fmt == 0) hipLaunchKernelGGL((moe_gate_up_kernel<0, MTMAX>), up, dim3(512), 0, stream, a, s);
+  else hipLaunchKernelGGL((moe_gate_up_kernel<1, MTMAX>), up, dim3(512), 0, stream, a, s);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+#define FGB_DOWN(SWF, OUT, NT, WK)                                                                              \
+  hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, MTMAX, NT, WK>), dim3((unsigned)(a.H / (16 * NT))), dim3(64 * WK), \
+                     (size_t)WK * a.T * 16 * NT * sizeof(float), stream, a, s)
+#define FGB_DOWN_TYPES(NT, WK)                            \
+  do {                                                    \
+    if (a.s_w_fmt == 0) {                                 \
+      if (a.y_dtype == 0) FGB_DOWN(0, 0, NT, WK);         \
+      else FGB_DOWN(0, 1, NT, WK);                        \
+    } else {                                              \
+      if (a.y_dtype == 0) FGB_DOWN(1, 0, NT, WK);         \
+      else FGB_DOWN(1, 1, NT, WK);                        \
+    }                                                     \
+  } while (0)
+  // two weight tiles per wave share each activation fragment, and two tiles' bytes are in flight; one
+  // where that would leave CUs without a workgroup (measured: H = 7168, 224 workgroups of 32 columns
+  // 20.2 us against 448 of 16 23.6 at 1 token, 86 against 139 at 64; H = 2048, 128 workgroups of 16
+  // columns 17.0 us against 64 of 32 24.5)
+  if (a.H / 32 >= 160) FGB_DOWN_TYPES(2, 8);
+  else FGB_DOWN_TYPES(1, 8);
+#undef FGB_DOWN_TYPES
+#undef FGB_DOWN
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_moe_ffn(const MoeArgs& a, void* workspace, hipStream_t stream) {
   Space s;
   layout(a.T, a.top_k, a.E, a.H, a.I, reinterpret_cast<uint8_t*>(workspace), &s);
-  hipLaunchKernelGGL(moe_prep_kernel, dim3((unsigned)(a.T * a.top_k)), dim3(PREP), 0, stream, a, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const dim3 up((unsigned)(a.I / 128), (unsigned)max_experts(a.T, a.top_k, a.E)), down((unsigned)(a.H / 32));
-  if (a.s_w_fmt == 0) hipLaunchKernelGGL(moe_gate_up_kernel<0>, up, dim3(512), 0, stream, a, s);
-  else hipLaunchKernelGGL(moe_gate_up_kernel<1>, up, dim3(512), 0, stream, a, s);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const size_t lds = (size_t)8 * a.T * 32 * sizeof(float);
-#define FGB_DOWN(SWF, OUT) hipLaunchKernelGGL((moe_down_kernel<SWF, OUT>), down, dim3(512), lds, stream, a, s)
-  if (a.s_w_fmt == 0) {
-    if (a.y_dtype == 0) FGB_DOWN(0, 0); else FGB_DOWN(0, 1);
-  } else {
-    if (a.y_dtype == 0) FGB_DOWN(1, 0); else FGB_DOWN(1, 1);
-  }
-#undef FGB_DOWN
-  return hipGetLastError();
+  if (a.T <= 16) return launch_layer<1>(a, s, stream);
+  if (a.T <= 32) return launch_layer<2>(a, s, stream);
+  return launch_layer<4>(a, s, stream);
 }
 
 }  // namespace fgb
