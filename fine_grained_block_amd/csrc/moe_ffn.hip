@@ -64,14 +64,40 @@ struct Space {
   float* xs;
   uint8_t* hq;
   float* hs;
+  float* hf;           // [experts * T, I]: the product itself, where the down launch quantizes it
 };
 
 int max_experts(int T, int top_k, int E) { return T * top_k < E ? T * top_k : E; }
-// sum over experts of ceil(rows / 16) <= (pairs + 15 experts) / 16
-int max_tiles(int T, int top_k, int E) { return T * top_k / kTile + max_experts(T, top_k, E); }
+
+// Whether the gate+up workgroups find their expert and quantize its rows themselves (no prep launch):
+// the rows' codes, T * H bytes at most, have to leave LDS for two workgroups per CU.  Measured on 7168 x
+// 2048, 32 experts, top 8, without and with the prep launch (all launches): 1 token 70.7 and 73.8 us, 7
+// tokens (50 KB of codes, one workgroup per CU) 171 and 168 us.
+constexpr int kFusedTokens = 32, kFusedBytes = 32 << 10;
+bool fused_prep(int T, int H) { return T <= kFusedTokens && T * H <= kFusedBytes; }
+
+// Whether the gated product is quantized by the down launch.  A gate+up workgroup of 128 columns (the
+// quantization group) leaves half the CUs idle when one or two tokens reach only a few experts, and a CU
+// takes in no more than about 16 bytes a clock whatever is in flight (128 workgroups: 5.0 TB/s with 3
+// or with 7 K-blocks ahead); workgroups of 64 columns write the float32 product and every down
+// workgroup quantizes all of it, which has to stay small.  Measured at 1 token (7168 x 2048, 32 experts,
+// top 8): gate+up 50.2 -> 40.5 us, down 20.5 -> 22.4 us.
+constexpr int kLateValues = 32 << 10, kLateBlocks = 62;
+bool late_quant(int T, int top_k, int E, int H, int I) {
+  return T <= kTile && fused_prep(T, H) && max_experts(T, top_k, E) * T * (I / 128) <= kLateValues / 128 &&
+         (I / 128 < 64 ? I / 128 : 64) * T <= kLateBlocks;
+}
+
+// Tiles of 16 rows: with the prep launch they are packed (sum over experts of ceil(rows / 16) <=
+// (pairs + 15 experts) / 16), without it every routed expert has room for all tokens.
+int expert_tiles(int T) { return (T + kTile - 1) / kTile; }
+int max_tiles(int T, int top_k, int E, int H) {
+  const int n = max_experts(T, top_k, E);
+  return fused_prep(T, H) ? n * expert_tiles(T) : T * top_k / kTile + n;
+}
 
 size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
-  const size_t tiles = (size_t)max_tiles(T, top_k, E), rows = tiles * kTile;
+  const size_t tiles = (size_t)max_tiles(T, top_k, E, H), rows = tiles * kTile;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -85,8 +111,10 @@ size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
   t.row_weight = (float*)take(rows * sizeof(float));
   t.xq = take((size_t)T * H);
   t.xs = (float*)take((size_t)T * (H / 128) * sizeof(float));
-  t.hq = take(rows * I);
-  t.hs = (float*)take(rows * (I / 128) * sizeof(float));
+  const bool late = late_quant(T, top_k, E, H, I);
+  t.hq = take(late ? 0 : rows * I);
+  t.hs = (float*)take(late ? 0 : rows * (I / 128) * sizeof(float));
+  t.hf = (float*)take(late ? (size_t)max_experts(T, top_k, E) * T * I * sizeof(float) : 0);
   if (s) *s = t;
   return at;
 }
@@ -214,34 +242,26 @@ __device__ __forceinline__ v8i codes8(const int4& lo, const int4& hi) {
 // D blocks in flight in registers.
 //   acc[n][m] += P * (s_a * s_w[n])   per K-block, P the block's product sums.
 // w[n]: lane address of weight tile n at the first block (row l/8, 16-byte chunk l%8), rows 8 further
-// at + 8 * pitch; a[m]: lane address of tile m's fragment; sa[m]: lane address of its row's scale;
-// `scale(n, kk)` gives the weight block's scale.  Lanes whose row does not exist are given the
-// addresses of one that does (the same lines: no traffic, no branch), and their results are dropped.
-// Blocks past the end are clamped to the last one, so the loads in flight are the same number in
-// every step.
-// ---------------------------------------------------------------------------------------------
-template <int NT, int MT, int D, typename Scale>
-__device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int64_t pitch, const uint8_t* const (&a)[MT],
-                                              const float* const (&sa)[MT], int nk, uint8_t* lds,
-                                              Scale scale, v4f (&acc)[NT][MT]) {
+// at + 8 * pitch; acts.load(kk, d) starts a block's activation loads, acts.start() runs once the first
+// blocks are on their way, acts.codes(kk, d, m) and acts.scale(kk, d, m) give tile m's fragment and the
+// scale of this lane's row; `scale(n, kk)` the weight block's.  Lanes whose row does not exist repeat
+// one that does, and their results are dropped.  Blocks past the end are clamped to the last one, so
+// the loads in flight are the same number in every step.
+template <int NT, int MT, int D, typename Acts, typename Scale>
+__device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int64_t pitch, Acts& acts, int nk,
+                                              uint8_t* lds, Scale scale, v4f (&acc)[NT][MT]) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wo0 = swz(lane >> 3, lane & 7), wo1 = swz((lane >> 3) + 8, lane & 7);
   const int ro0 = swz(r, 2 * g), ro1 = swz(r, 2 * g + 1);
-  int4 wv[D][NT][2], av[D][MT][2];
-  float sv[D][MT];
+  int4 wv[D][NT][2];
   auto load = [&](int kk, int d) {
-    const int64_t wk = (int64_t)kk * 128, ak = (int64_t)kk * kFrag;
+    const int64_t wk = (int64_t)kk * 128;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       wv[d][n][0] = gload_i4_last(w[n] + wk);
       wv[d][n][1] = gload_i4_last(w[n] + 8 * pitch + wk);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      av[d][m][0] = gload_i4(a[m] + ak);
-      av[d][m][1] = gload_i4(a[m] + ak + 1024);
-      sv[d][m] = gload<float>(sa[m] + kk * kTile);
-    }
+    acts.load(kk, d);
   };
   auto compute = [&](int kk, int d) {
 #pragma unroll
@@ -254,7 +274,7 @@ __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int
     }
     v8i af[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) af[m] = codes8(av[d][m][0], av[d][m][1]);
+    for (int m = 0; m < MT; ++m) af[m] = acts.codes(kk, d, m);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint8_t* t = lds + n * kFrag;
@@ -262,7 +282,7 @@ __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int
       const float sw = scale(n, kk);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        acc[n][m] += mfma_e4m3_16x16x128(wf, af[m]) * (sv[d][m] * sw);
+        acc[n][m] += mfma_e4m3_16x16x128(wf, af[m]) * (acts.scale(kk, d, m) * sw);
         asm volatile("" : "+v"(acc[n][m]));
       }
     }
@@ -270,6 +290,7 @@ __device__ __forceinline__ void stream_blocks(const uint8_t* const (&w)[NT], int
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) load(min(d, nk - 1), d);
   __builtin_amdgcn_sched_barrier(0);
+  acts.start();
   int kk = 0;
   for (; kk + D <= nk; kk += D) {
 #pragma unroll
@@ -330,24 +351,104 @@ __device__ __forceinline__ void lds_barrier() {
 // ---------------------------------------------------------------------------------------------
 constexpr int CH = 4;  // K-blocks per chunk and weight blocks in registers per wave
 
-template <int SWF, int MTMAX>
+struct Routed {
+  int e, tile0, rows;  // expert, its first tile, its rows; e < 0: the workgroup has none
+};
+
+// FUSED: every workgroup finds routed expert number `n` (in ascending order) and its tokens from the ids:
+// a bit per expert, the n-th set bit, then the pairs that name it, in order, a token once.  `tokens`
+// gets the rows' tokens.  The workgroups of column 0 write the expert's table entries for the down launch.
+__device__ __forceinline__ Routed find_expert(const MoeArgs& p, const Space& s, int n, bool writes, int* sid,
+                                              uint32_t* bits, int* tokens) {
+  const int tid = threadIdx.x, lane = tid & 63, P = p.T * p.top_k;
+  if (tid < kMoeMaxExperts / 32) bits[tid] = 0;
+  for (int q = tid; q < P; q += 512) sid[q] = gload<int>(p.ids + q);
+  __syncthreads();
+  for (int q = tid; q < P; q += 512) {
+    const int id = sid[q];
+    if (id >= 0 && id < p.E) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  const uint32_t word = lane < kMoeMaxExperts / 32 ? bits[lane] : 0u;
+  const int count = __popc(word);
+  int inc = count;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  const int active = __builtin_amdgcn_readlane(inc, 31);
+  if (writes && n == 0 && tid == 0) *s.active = active;
+  if (n >= active) return Routed{-1, 0, 0};
+  const int w = __ffsll((long long)__ballot(inc > n && inc - count <= n)) - 1;
+  uint32_t left = (uint32_t)__builtin_amdgcn_readlane((int)word, w);
+  for (int skip = n - __builtin_amdgcn_readlane(inc - count, w); skip > 0; --skip) left &= left - 1;
+  Routed ex{32 * w + __ffs((int)left) - 1, n * ((p.T + kTile - 1) / kTile), 0};
+  for (int c = 0; c < P; c += 64) {
+    const int q = c + lane;
+    bool keep = q < P && sid[q] == ex.e;
+    const int t = q / p.top_k;
+    for (int f = t * p.top_k; keep && f < q; ++f) keep = sid[f] != ex.e;
+    const unsigned long long mask = __ballot(keep);
+    if (keep) {
+      const int row = ex.rows + __popcll(mask & ((1ull << lane) - 1));
+      tokens[row] = t;  // (all waves write the same)
+      if (writes && tid < 64) {
+        float sum = 0.0f;  // with the weights of later pairs of the token that name the same expert
+        for (int f = q; f < (t + 1) * p.top_k; ++f)
+          if (sid[f] == ex.e) sum += gload<float>(p.weights + f);
+        s.row_token[ex.tile0 * kTile + row] = t;
+        s.row_weight[ex.tile0 * kTile + row] = sum;
+      }
+    }
+    ex.rows += __popcll(mask);
+  }
+  if (writes && tid == 0) s.experts[n] = make_int4(ex.e, ex.tile0, ex.rows, 0);
+  return ex;
+}
+
+template <int SWF, int MTMAX, bool FUSED, int COLS = 128>
 __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s) {
+  static_assert(!FUSED || MTMAX * kTile <= kFusedTokens, "few tokens");
+  static_assert(COLS == 128 || (COLS == 64 && FUSED && MTMAX == 1), "half groups: quantized by the down launch");
+  constexpr int CT = COLS / 16;  // column tiles; 64 columns: two waves each, splitting the K-blocks
   __shared__ __attribute__((aligned(1024))) uint8_t wtiles[8][2 * kFrag];
-  __shared__ __attribute__((aligned(1024))) uint8_t atiles[2][CH * MTMAX * kFrag];
-  __shared__ float ascale[2][CH][MTMAX * kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t atiles[2][FUSED ? 16 : CH * MTMAX * kFrag];
+  __shared__ float ascale[2][CH][FUSED ? 1 : MTMAX * kTile];
   __shared__ float sws[2][256];  // the two weight block rows' scales (H <= 32768)
   __shared__ float amax[8][MTMAX * kTile];
-  if ((int)blockIdx.y >= gload<int>(s.active)) return;
+  // FUSED: the expert's rows, codes [H/128][T][128] (16-byte chunks swizzled by row) and scales [H/128][T]
+  extern __shared__ __attribute__((aligned(1024))) uint8_t xrows[];
+  __shared__ int sid[FUSED ? kMoeMaxPairs : 1];
+  __shared__ uint32_t bits[FUSED ? kMoeMaxExperts / 32 : 1];
+  __shared__ int tokens[FUSED ? kFusedTokens : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const v4i ex = gload<v4i>(s.experts + blockIdx.y);
-  const int e = __builtin_amdgcn_readfirstlane(ex[0]), tile0 = __builtin_amdgcn_readfirstlane(ex[1]);
-  const int rows = __builtin_amdgcn_readfirstlane(ex[2]);
-  const int KB = p.H / 128, NB = p.I / 128, gb = blockIdx.x;
+  int e, tile0, rows;
+  if constexpr (FUSED) {
+    const Routed ex = find_expert(p, s, blockIdx.y, blockIdx.x == 0, sid, bits, tokens);
+    if (ex.e < 0) return;
+    e = ex.e;
+    tile0 = ex.tile0;
+    rows = ex.rows;
+  } else {
+    // (the entry is loaded with the count, not after it: a workgroup past the count drops it)
+    const int active = gload<int>(s.active);
+    const v4i ex = gload<v4i>(s.experts + blockIdx.y);
+    if ((int)blockIdx.y >= active) return;
+    e = ex[0];
+    tile0 = ex[1];
+    rows = ex[2];
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  tile0 = __builtin_amdgcn_readfirstlane(tile0);
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  const int KB = p.H / 128, NB = p.I / 128, gb = blockIdx.x * COLS / 128;
+  const int ct = wave % CT, kbeg = wave / CT * ((KB + 1) / 2), kend = COLS == 64 && wave < CT ? (KB + 1) / 2 : KB;
   // this lane's weight bytes from the expert's first: 32-bit offsets (2 I H <= 2^31), the K-block is the
   // buffer load's scalar offset
-  const uint32_t wrow = (uint32_t)((gb * 128 + wave * 16 + (lane >> 3)) * p.H + 16 * (lane & 7));
+  const uint32_t wrow = (uint32_t)((blockIdx.x * COLS + ct * 16 + (lane >> 3)) * p.H + 16 * (lane & 7));
   const uint32_t up = (uint32_t)p.I * p.H, pitch8 = 8u * p.H;
   const uint32_t woff[4] = {wrow, wrow + pitch8, wrow + up, wrow + up + pitch8};
   const uint8_t* const wexp = p.w13_q + (int64_t)e * 2 * p.I * p.H;
@@ -359,9 +460,10 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     constexpr int MT = decltype(mt_c)::value;
     // weights: blocks past the end repeat the last one (their scale is 0)
     int4 wv[CH][2][2];
+    auto block = [&](int kk) { return COLS == 128 ? min(kk, KB - 1) : max(min(kbeg + kk, kend - 1), 0); };
     auto load = [&](int kk, int d) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wv[d][i / 2][i % 2] = bload16<kLastReadAux>(wexp, woff[i], (uint32_t)min(kk, KB - 1) * 128);
+      for (int i = 0; i < 4; ++i) wv[d][i / 2][i % 2] = bload16<kLastReadAux>(wexp, woff[i], (uint32_t)block(kk) * 128);
     };
     // activations: a chunk is CH * 128 contiguous bytes of each row; copy i of a thread takes 16 of them
     // (rows past the count repeat the last one)
@@ -370,17 +472,28 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     int4 av[NA];
     float sv = 0.0f;
     const int ak = tid % RC / 8, ac = tid & 7, ar = tid / RC;
-    uint32_t aoff[NA];
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      aoff[i] = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(i * RPC + ar, rows - 1)) * p.H + 16 * ac;
+    uint32_t aoff[NA], soff = 0;
     const int sk = tid / (MT * kTile), sr = tid % (MT * kTile);  // scale of row sr, block sk < CH
-    const uint32_t soff = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(sr, rows - 1)) * KB * 4;
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+        aoff[i] = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(i * RPC + ar, rows - 1)) * p.H + 16 * ac;
+      soff = (uint32_t)gload<int>(s.row_token + tile0 * kTile + min(sr, rows - 1)) * KB * 4;
+    }
     auto fetch = [&](int k0) {
 #pragma unroll
       for (int i = 0; i < NA; ++i) av[i] = bload16<0>(s.xq, aoff[i] + min(k0 + ak, KB - 1) * 128, 0);
       sv = bload4(s.xs, soff + min(k0 + min(sk, CH - 1), KB - 1) * 4);
     };
+    float* const xscale = reinterpret_cast<float*>(xrows + p.T * p.H);
+    // this lane's rows (FUSED; rows past the count repeat the last one)
+    int fq[MT], flo[MT], fhi[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      fq[m] = min(m * kTile + r, rows - 1);
+      flo[m] = swz(fq[m], 2 * g);
+      fhi[m] = swz(fq[m], 2 * g + 1);
+    }
     auto stash = [&](int k0, int buf) {
 #pragma unroll
       for (int i = 0; i < NA; ++i) {
@@ -405,24 +518,33 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
       }
       Wide wf[2];
       float sw[2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      auto weights = [&](int n) {
         wf[n] = widen(*reinterpret_cast<const int4*>(wt + n * kFrag + ro0), *reinterpret_cast<const int4*>(wt + n * kFrag + ro1));
-        sw[n] = sws[n][min(kk, KB - 1)];
+        sw[n] = sws[n][block(kk)];
+      };
+      // (one activation tile: the weight tiles are widened one after the other, which keeps the kernel
+      // within the registers of two workgroups per CU)
+      if constexpr (MT > 1) {
+        weights(0);
+        weights(1);
       }
-      const uint8_t* t = &atiles[buf][d * MT * kFrag];
+      const uint8_t* const t = FUSED ? xrows + block(kk) * p.T * 128 : &atiles[buf][d * MT * kFrag];
       const int lo = (g * 16 + (r ^ (2 * g + 8 * (d & 1)))) * 16, hi = 1024 + (g * 16 + (r ^ (2 * g + 1 + 8 * (d & 1)))) * 16;
-      int4 alo = *reinterpret_cast<const int4*>(t + lo), ahi = *reinterpret_cast<const int4*>(t + hi);
+      auto half = [&](int m, bool second) {
+        return *reinterpret_cast<const int4*>(t + (FUSED ? (second ? fhi[m] : flo[m]) : m * kFrag + (second ? hi : lo)));
+      };
+      int4 alo = half(0, false), ahi = half(0, true);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const Wide af = widen(alo, ahi);
-        const float sa = ascale[buf][d][m * kTile + r];
+        const float sa = FUSED ? (kbeg + kk < kend ? xscale[block(kk) * p.T + fq[m]] : 0.0f) : ascale[buf][d][m * kTile + r];
         if (m + 1 < MT) {
-          alo = *reinterpret_cast<const int4*>(t + (m + 1) * kFrag + lo);
-          ahi = *reinterpret_cast<const int4*>(t + (m + 1) * kFrag + hi);
+          alo = half(m + 1, false);
+          ahi = half(m + 1, true);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
+          if constexpr (MT == 1) weights(n);
           acc[n][m] += block_sum(wf[n], af) * (sa * sw[n]);
           // (the sum is due here: left alone, the compiler keeps every block's product sums to the end
           // of the chunk, in the registers that the weights in flight need)
@@ -432,18 +554,29 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     };
 #pragma unroll
     for (int d = 0; d < CH - 1; ++d) load(d, d);
-    fetch(0);
+    if constexpr (!FUSED) fetch(0);
     __builtin_amdgcn_sched_barrier(0);
     const int64_t sw0 = ((int64_t)e * 2 * NB + gb) * KB;
     for (int k = tid; k < KB; k += 512) {
       sws[0][k] = load_sw<SWF>(p.s_w13, sw0 + k);
       sws[1][k] = load_sw<SWF>(p.s_w13, sw0 + (int64_t)NB * KB + k);
     }
-    stash(0, 0);
+    if constexpr (FUSED) {
+      const int chunks = p.H / 16;
+      for (int i = tid; i < rows * chunks; i += 512) {
+        const int q = i / chunks, c = i - q * chunks;
+        float sc;
+        const int4 codes = quant_chunk(p.x + (int64_t)tokens[q] * p.ldx, c, sc);
+        *reinterpret_cast<int4*>(xrows + c / 8 * p.T * 128 + swz(q, c % 8)) = codes;
+        if (c % 8 == 0) xscale[c / 8 * p.T + q] = sc;
+      }
+    } else {
+      stash(0, 0);
+    }
     lds_barrier();
     int buf = 0;
-    for (int k0 = 0; k0 < KB; k0 += CH) {
-      fetch(k0 + CH);  // (past the end: the last block again, stashed where nothing reads it)
+    for (int k0 = 0; k0 < kend - kbeg; k0 += CH) {
+      if constexpr (!FUSED) fetch(k0 + CH);  // (past the end: the last block again, stashed where nothing reads it)
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < CH; ++d) {
@@ -453,9 +586,29 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
         compute(k0 + d, d, buf);
         __builtin_amdgcn_sched_barrier(0);
       }
-      stash(k0 + CH, buf ^ 1);
-      lds_barrier();
-      buf ^= 1;
+      if constexpr (!FUSED) {
+        stash(k0 + CH, buf ^ 1);
+        lds_barrier();
+        buf ^= 1;
+      }
+    }
+    if constexpr (COLS == 64) {
+      // the two K halves, the gated product, float32
+      v4f* const red = reinterpret_cast<v4f*>(wtiles);
+      __syncthreads();  // (the weight tiles are free)
+      if (wave >= CT) {
+        red[(ct * 2 + 0) * 64 + lane] = acc[0][0];
+        red[(ct * 2 + 1) * 64 + lane] = acc[1][0];
+      }
+      __syncthreads();
+      if (wave < CT && r < rows) {
+        const v4f gate = acc[0][0] + red[(ct * 2 + 0) * 64 + lane], u = acc[1][0] + red[(ct * 2 + 1) * 64 + lane];
+        float v[4] = {gate[0], gate[1], gate[2], gate[3]};
+        activate<4>(p.act, v);
+        gstore<v4f>(s.hf + ((int64_t)blockIdx.y * p.T + r) * p.I + blockIdx.x * COLS + ct * 16 + 4 * g,
+                    v4f{v[0] * u[0], v[1] * u[1], v[2] * u[2], v[3] * u[3]});
+      }
+      return;
     }
     // the gated product of this wave's 16 columns (lane: row r, columns 4 g .. 4 g + 3) and the rows'
     // maxima over the workgroup's 128 columns
@@ -494,15 +647,78 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
   else run(std::integral_constant<int, MTMAX < 4 ? 1 : 4>{});
 }
 
+// Activations of the down products: the quantized product's fragments from the workspace ...
+template <int MT, int D>
+struct StoredActs {
+  const uint8_t* a[MT];   // lane address of tile m's fragment at the first block
+  const float* sa[MT];    // and of its row's scale
+  int4 av[D][MT][2];
+  float sv[D][MT];
+  __device__ __forceinline__ void load(int kk, int d) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      av[d][m][0] = gload_i4(a[m] + (int64_t)kk * kFrag);
+      av[d][m][1] = gload_i4(a[m] + (int64_t)kk * kFrag + 1024);
+      sv[d][m] = gload<float>(sa[m] + kk * kTile);
+    }
+  }
+  __device__ __forceinline__ void start() {}
+  __device__ __forceinline__ v8i codes(int, int d, int m) const { return codes8(av[d][m][0], av[d][m][1]); }
+  __device__ __forceinline__ float scale(int, int d, int m) const { return sv[d][m]; }
+};
+
+// ... or the product's float32 rows, quantized by the wave for its own K-blocks: 8 lanes per 128-group,
+// 16 values each; codes [block][T][128], chunks swizzled by row, and scales [block][T] in LDS.
+struct LateActs {
+  const float* h;  // row 0 at the first block
+  int64_t pitch;
+  int T, rows, nk, q;  // q: this lane's row
+  uint8_t* codes_lds;
+  float* scale_lds;
+  __device__ __forceinline__ void load(int, int) {}
+  __device__ __forceinline__ void start() {
+    const int lane = threadIdx.x & 63;
+    for (int i = lane >> 3; i < nk * rows; i += 8) {  // (whole 8-lane groups)
+      const int kk = i / rows, row = i - kk * rows;
+      const float* src = h + row * pitch + kk * 128 + 16 * (lane & 7);
+      float v[16], mx = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const v4f t = gload<v4f>(src + 4 * u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[4 * u + j] = t[j];
+          mx = fmaxf(mx, fabsf(t[j]));
+        }
+      }
+      const float sc = row8_max(mx) * kInvMax;
+      int4 c;
+      c.x = codes4(v[0], v[1], v[2], v[3], sc);
+      c.y = codes4(v[4], v[5], v[6], v[7], sc);
+      c.z = codes4(v[8], v[9], v[10], v[11], sc);
+      c.w = codes4(v[12], v[13], v[14], v[15], sc);
+      *reinterpret_cast<int4*>(codes_lds + kk * T * 128 + swz(row, lane & 7)) = c;
+      if ((lane & 7) == 0) scale_lds[kk * T + row] = sc;
+    }
+  }
+  __device__ __forceinline__ v8i codes(int kk, int, int) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const uint8_t* t = codes_lds + kk * T * 128;
+    return codes8(*reinterpret_cast<const int4*>(t + swz(q, 2 * g)), *reinterpret_cast<const int4*>(t + swz(q, 2 * g + 1)));
+  }
+  __device__ __forceinline__ float scale(int kk, int, int) const { return scale_lds[kk * T + q]; }
+};
+
 // ---------------------------------------------------------------------------------------------
 // down: grid H / (16 NT), WK waves.  The K-blocks of all routed experts, in expert order, are one list
 // that the waves split evenly; a wave walks its share expert by expert (segments).
 // ---------------------------------------------------------------------------------------------
-template <int SWF, int OUT, int MTMAX, int NT, int WK>
+template <int SWF, int OUT, int MTMAX, int NT, int WK, bool LATE>
 __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
   constexpr int COLS = 16 * NT;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WK][NT * kFrag];
-  extern __shared__ __attribute__((aligned(16))) float ysum[];  // [WK waves][T][COLS]
+  // [WK waves][T][COLS]; LATE: then each wave's codes and scales of a segment
+  extern __shared__ __attribute__((aligned(16))) float ysum[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -511,6 +727,9 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
   float* const mine = ysum + wave * p.T * COLS;
   for (int i = lane; i < p.T * (COLS / 4); i += 64) *reinterpret_cast<v4f*>(mine + 4 * i) = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // lane l holds the table entries of routed expert l (loaded with the count; entries past it are not
+  // used), later ones are loaded when they come up
+  const v4i table = gload<v4i>(s.experts + min(lane, min(p.T * p.top_k, p.E) - 1));
   const int units = gload<int>(s.active) * KB;
   const int per = (units + WK - 1) / WK;
   int u = __builtin_amdgcn_readfirstlane(min(units, wave * per));
@@ -518,9 +737,17 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
   while (u < u1) {
     const int si = u / KB, kb0 = u - si * KB;
     const int nk = min(min(KB - kb0, u1 - u), 64);
-    const v4i ex = gload<v4i>(s.experts + si);
-    const int e = __builtin_amdgcn_readfirstlane(ex[0]), tile0 = __builtin_amdgcn_readfirstlane(ex[1]);
-    const int rows = __builtin_amdgcn_readfirstlane(ex[2]);
+    int e, tile0, rows;
+    if (si < 64) {
+      e = __builtin_amdgcn_readlane(table[0], si);
+      tile0 = __builtin_amdgcn_readlane(table[1], si);
+      rows = __builtin_amdgcn_readlane(table[2], si);
+    } else {
+      const v4i ex = gload<v4i>(s.experts + si);
+      e = __builtin_amdgcn_readfirstlane(ex[0]);
+      tile0 = __builtin_amdgcn_readfirstlane(ex[1]);
+      rows = __builtin_amdgcn_readfirstlane(ex[2]);
+    }
     const float swl = lane < nk ? load_sw<SWF>(p.s_w2, ((int64_t)e * NB + n0 / 128) * KB + kb0 + lane) : 0.0f;
     const uint8_t* w0 = p.w2_q + ((int64_t)e * p.H + n0 + (lane >> 3)) * p.I + (int64_t)kb0 * 128 + 16 * (lane & 7);
     const uint8_t* w[NT];
@@ -529,20 +756,41 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
     auto run = [&](auto mt_c) {
       constexpr int MT = decltype(mt_c)::value;
       constexpr int D = 3;  // blocks in registers (4: 2-8% slower with one row tile, registers; 2: 5% with four)
-      const uint8_t* a[MT];
-      const float* sa[MT];
+      std::conditional_t<LATE, LateActs, StoredActs<MT, D>> acts;
+      if constexpr (LATE) {
+        const int seg = min(KB, 64);
+        uint8_t* const mem = reinterpret_cast<uint8_t*>(ysum + WK * p.T * COLS) + wave * seg * p.T * 132;
+        acts.h = s.hf + (int64_t)si * p.T * p.I + kb0 * 128;
+        acts.pitch = p.I;
+        acts.T = p.T;
+        acts.rows = rows;
+        acts.nk = nk;
+        acts.q = min(r, rows - 1);
+        acts.codes_lds = mem;
+        acts.scale_lds = reinterpret_cast<float*>(mem + seg * p.T * 128);
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int q = min(m * kTile + r, rows - 1);
+          acts.a[m] = s.hq + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kFrag + (g * kTile + q % kTile) * 16;
+          acts.sa[m] = s.hs + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kTile + q % kTile;
+        }
+      }
+      // the rows' tokens and weights, needed at the segment's end
+      int token[MT];
+      float weight[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int q = min(m * kTile + r, rows - 1);
-        a[m] = s.hq + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kFrag + (g * kTile + q % kTile) * 16;
-        sa[m] = s.hs + ((int64_t)(tile0 + q / kTile) * KB + kb0) * kTile + q % kTile;
+        const int row = tile0 * kTile + min(m * kTile + r, rows - 1);
+        token[m] = gload<int>(s.row_token + row);
+        weight[m] = gload<float>(s.row_weight + row);
       }
       v4f acc[NT][MT];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[n][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      stream_blocks<NT, MT, D>(w, p.I, a, sa, nk, &tiles[wave][0],
+      stream_blocks<NT, MT, D>(w, p.I, acts, nk, &tiles[wave][0],
                               [&](int, int kk) {
                                 return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), kk));
                               }, acc);
@@ -550,13 +798,10 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (m * kTile + r < rows) {
-          const int row = (tile0 + m) * kTile + r;
-          const int t = gload<int>(s.row_token + row);
-          const float wt = gload<float>(s.row_weight + row);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            v4f* const q = reinterpret_cast<v4f*>(mine + t * COLS + n * 16 + 4 * g);
-            *q += acc[n][m] * wt;
+            v4f* const q = reinterpret_cast<v4f*>(mine + token[m] * COLS + n * 16 + 4 * g);
+            *q += acc[n][m] * weight[m];
           }
         }
       }
@@ -590,19 +835,40 @@ size_t moe_ffn_workspace_bytes(int T, int top_k, int E, int H, int I) {
 
 namespace {
 
+template <int MTMAX, bool FUSED, int COLS>
+void launch_gate_up(const MoeArgs& a, const Space& s, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.I / COLS), (unsigned)max_experts(a.T, a.top_k, a.E)), block(512);
+  const size_t lds = FUSED ? (size_t)a.T * (a.H + a.H / 128 * sizeof(float)) : 0;
+  if (a.s_w_fmt == 0) hipLaunchKernelGGL((moe_gate_up_kernel<0, MTMAX, FUSED, COLS>), grid, block, lds, stream, a, s);
+  else hipLaunchKernelGGL((moe_gate_up_kernel<1, MTMAX, FUSED, COLS>), grid, block, lds, stream, a, s);
+}
+
 template <int MTMAX>
 hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
-  hipLaunchKernelGGL(moe_prep_kernel, dim3((unsigned)a.T + 1), dim3(PREP), 0, stream, a, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const dim3 up((unsigned)(a.I / 128), (unsigned)max_experts(a.T, a.top_k, a.E));
-  if (a.s_w_fmt == 0) hipLaunchKernelGGL((moe_gate_up_kernel<0, MTMAX>), up, dim3(512), 0, stream, a, s);
-  else hipLaunchKernelGGL((moe_gate_up_kernel<1, MTMAX>), up, dim3(512), 0, stream, a, s);
+  hipError_t e;
+  const bool late = late_quant(a.T, a.top_k, a.E, a.H, a.I);
+  if (MTMAX == 1 && late) {
+    launch_gate_up<1, true, 64>(a, s, stream);
+  } else if (MTMAX * kTile <= kFusedTokens && fused_prep(a.T, a.H)) {
+    launch_gate_up<MTMAX * kTile <= kFusedTokens ? MTMAX : 1, true, 128>(a, s, stream);
+  } else {
+    hipLaunchKernelGGL(moe_prep_kernel, dim3((unsigned)a.T + 1), dim3(PREP), 0, stream, a, s);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    launch_gate_up<MTMAX, false, 128>(a, s, stream);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-#define FGB_DOWN(SWF, OUT, NT, WK)                                                                              \
-  hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, MTMAX, NT, WK>), dim3((unsigned)(a.H / (16 * NT))), dim3(64 * WK), \
-                     (size_t)WK * a.T * 16 * NT * sizeof(float), stream, a, s)
+  // (late: one activation tile, T <= 16)
+  const size_t extra = late ? (size_t)8 * (a.I / 128 < 64 ? a.I / 128 : 64) * a.T * 132 : 0;
+#define FGB_DOWN_LATE(SWF, OUT, NT, WK, LATE)                                                                     \
+  hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, LATE ? 1 : MTMAX, NT, WK, LATE>), dim3((unsigned)(a.H / (16 * NT))), \
+                     dim3(64 * WK), (size_t)WK * a.T * 16 * NT * sizeof(float) + extra, stream, a, s)
+#define FGB_DOWN(SWF, OUT, NT, WK)                            \
+  do {                                                        \
+    if (MTMAX == 1 && late) FGB_DOWN_LATE(SWF, OUT, NT, WK, true); \
+    else FGB_DOWN_LATE(SWF, OUT, NT, WK, false);              \
+  } while (0)
 #define FGB_DOWN_TYPES(NT, WK)                            \
   do {                                                    \
     if (a.s_w_fmt == 0) {                                 \
@@ -621,6 +887,7 @@ hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
   else FGB_DOWN_TYPES(1, 8);
 #undef FGB_DOWN_TYPES
 #undef FGB_DOWN
+#undef FGB_DOWN_LATE
   return hipGetLastError();
 }
 

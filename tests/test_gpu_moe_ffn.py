@@ -72,6 +72,7 @@ def _run(dev, T, E, k, H, I, fmt="f32", act="silu", kind="random", seed=0, **kw)
 SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (1, 32, 8, 1024, 512), (2, 4, 2, 128, 1152), (3, 16, 16, 384, 256),
           (7, 32, 8, 1024, 256), (16, 8, 2, 512, 512), (17, 3, 1, 256, 256), (33, 5, 2, 640, 384), (64, 32, 8, 512, 256),
           (64, 64, 16, 256, 128), (49, 1, 1, 256, 512), (64, 300, 4, 128, 128), (5, 1024, 3, 128, 128),
+          (9, 6, 3, 4096, 256), (20, 6, 3, 2048, 256), (4, 8, 8, 1024, 1152), (16, 8, 1, 128, 256), (3, 70, 24, 256, 128),
           (2, 2, 1, 8320, 128), (2, 2, 2, 128, 9600), (1, 1, 1, 32768, 128), (1, 1, 1, 128, 32768)]
 
 
@@ -84,9 +85,11 @@ def test_moe_matches_oracle(dev, T, E, k, H, I, fmt):
 
 
 @pytest.mark.parametrize("T", [15, 16, 17, 31, 32, 33, 48, 49, 63, 64])
-def test_one_popular_expert(dev, T):
-    """All tokens in one expert: one to four activation tiles, the last one full or ragged."""
-    y, x, ids, w, ops, _ = _run(dev, T, 5, 2, 384, 256, kind="one", seed=2)
+@pytest.mark.parametrize("H", [384, 2304])
+def test_one_popular_expert(dev, T, H):
+    """All tokens in one expert: one to four activation tiles, the last one full or ragged; short rows
+    (quantized where they are used) and longer ones (by the launch before)."""
+    y, x, ids, w, ops, _ = _run(dev, T, 5, 2, H, 256, kind="one", seed=2)
     _check(y, x, ids, w, ops, "f32", "silu")
 
 
