@@ -83,15 +83,18 @@ def _dense(t: torch.Tensor, name: str, dtypes, shape: tuple) -> None:
 def _on_device(*named) -> None:
     """Every tensor lives on the current HIP device (checked after the shapes, so that shape
     errors are reported without touching the device)."""
-    cur = None
+    cur = -1
     for name, t in named:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()  # -1: host memory
+        if at == cur and cur >= 0:
+            continue
+        if at < 0:
             raise ValueError(f"{name} must be on the GPU, got {t.device}")
-        if cur is None:
+        if cur < 0:
             cur = torch.cuda.current_device()
-        if t.get_device() != cur:
+        if at != cur:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
 
 
@@ -377,10 +380,10 @@ def gemm_epilogue(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: 
         workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().fgb_w8a8_block_gemm_epilogue(
-        _ptr(a_q), _row_ld(a_q), _ptr(s_a), s_a.stride(0), _ptr(w_q), _ptr(s_w), _scale_fmt(s_w),
+        _ptr(a_q), a_q.stride(0), _ptr(s_a), s_a.stride(0), _ptr(w_q), _ptr(s_w), _scale_fmt(s_w),
         _ptr(bias), 0 if bias is None else _out_code(bias.dtype), act,
         _ptr(residual), 0 if residual is None else _out_code(residual.dtype),
-        0 if residual is None else _row_ld(residual), _ptr(out), _out_code(out.dtype), _row_ld(out), M, N, K,
+        0 if residual is None else residual.stride(0), _ptr(out), _out_code(out.dtype), out.stride(0), M, N, K,
         _ptr(workspace), ws_bytes, _stream())
     check("fgb_w8a8_block_gemm_epilogue", st)
     return out
@@ -462,7 +465,7 @@ def moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", select
         _dense(ids, "ids", (torch.int32,), (T, top_k))
         _dense(weights, "weights", (torch.float32,), (T, top_k))
         _on_device(("logits", logits), ("select_bias", select_bias), ("ids", ids), ("weights", weights))
-    st = lib().fgb_moe_route(_ptr(logits), _out_code(logits.dtype), _row_ld(logits), T, E, top_k, score,
+    st = lib().fgb_moe_route(_ptr(logits), _out_code(logits.dtype), logits.stride(0), T, E, top_k, score,
                              _ptr(select_bias), int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights),
                              _stream())
     check("fgb_moe_route", st)
@@ -521,11 +524,11 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_q: to
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().fgb_moe_ffn(_ptr(x), _row_ld(x), _ptr(ids), _ptr(weights), top_k, _ptr(w13_q), _ptr(s_w13), _ptr(w2_q),
+    st = lib().fgb_moe_ffn(_ptr(x), x.stride(0), _ptr(ids), _ptr(weights), top_k, _ptr(w13_q), _ptr(s_w13), _ptr(w2_q),
                            _ptr(s_w2), _scale_fmt(s_w13), E, act, _ptr(residual),
                            0 if residual is None else _out_code(residual.dtype),
-                           0 if residual is None else _row_ld(residual), _ptr(out), _out_code(out.dtype),
-                           _row_ld(out), T, H, I, _ptr(workspace), ws_bytes, _stream())
+                           0 if residual is None else residual.stride(0), _ptr(out), _out_code(out.dtype),
+                           out.stride(0), T, H, I, _ptr(workspace), ws_bytes, _stream())
     check("fgb_moe_ffn", st)
     return out
 

