@@ -468,13 +468,39 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
     }
   }
 
+  bool staged_f32 = false;
   if constexpr (Args::kEpilogue) {
-    // The float32 sums go through LDS (all stages, free once every wave is past its last block),
-    // so that each thread finishes 8 consecutive outputs of a row: one 16-byte residual load and
-    // one 16-byte store per bf16 group, whole lines per wave, and the activation once per value in
-    // a thread whose column group, hence bias, is the same in every iteration.  Staged as float32
-    // because y is rounded once, after the residual is added.  16-byte chunk c of row r sits at
-    // c ^ (r & 15): the 16 rows of a fragment write to distinct banks.
+    // Without a residual, bias and activation are applied to the sums where they are (lane: four
+    // consecutive output features per MFMA tile), and the tile leaves like the plain GEMM's (4096 x
+    // 28672 x 4096, plain 387 us: 395 with nothing to apply, 399 bias, 414 bias and silu, 444 bias and
+    // gelu; 2048 x 7168 x 2048, one tile per CU: staged as float32 31.8 us, like this 30.0).
+    staged_f32 = p.ep.residual != nullptr;
+    if (!staged_f32) {
+      if (p.ep.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < C::TN; ++i) {
+          float b[4];
+          load_values<4>(p.ep.bias, p.ep.bias_dtype, n0 + wn * (C::BN / C::WN) + i * 16 + 4 * (lane >> 4), b);
+#pragma unroll
+          for (int j = 0; j < C::TM; ++j) acc[i][j] += v4f{b[0], b[1], b[2], b[3]};
+        }
+      }
+      with_activation(p.ep.act, [&](auto fn) {
+#pragma unroll
+        for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+          for (int j = 0; j < C::TM; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][j][q] = fn(acc[i][j][q]);
+      });
+    }
+  }
+  if constexpr (Args::kEpilogue) if (staged_f32) {
+    // With a residual, the float32 sums go through LDS (all stages, free once every wave is past its
+    // last block), so that each thread finishes 8 consecutive outputs of a row: one 16-byte residual
+    // load and one 16-byte store per bf16 group, whole lines per wave, the bias of its column group in
+    // registers.  Staged as float32 because y is rounded once, after the residual is added.  16-byte
+    // chunk c of row r sits at c ^ (r & 15): the 16 rows of a fragment write to distinct banks.
     constexpr int ROWF = C::BN * 4;
     constexpr int RPS = C::STAGE / ROWF / 16 * 16;                             // rows per stage
     constexpr int RPR = RPS * C::STAGES < C::BM ? RPS * C::STAGES : C::BM;     // rows per round
@@ -490,13 +516,15 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
     const int64_t ncol = n0 + ch * 8;
     float bias[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (p.ep.bias != nullptr) load_values<8>(p.ep.bias, p.ep.bias_dtype, ncol, bias);
-    const bool res16 = p.ep.residual != nullptr && p.ep.residual_dtype == 0;
-    const bool res32 = p.ep.residual != nullptr && p.ep.residual_dtype != 0;
+    const bool res16 = p.ep.residual_dtype == 0, res32 = !res16;
     const int wrow = wm * (C::BM / C::WM);
 #pragma unroll
     for (int r = 0; r < C::BM / RPR; ++r) {
       // this round's bf16 residual goes out before the barriers (float32 residuals, twice the
-      // registers, are loaded where they are added)
+      // registers, are loaded where they are added).  All tiles of a wave of workgroups end together, so
+      // at 256 x 256 tiles these loads are the price of a residual (4096 x 28672 x 4096: 395 us without,
+      // 459 with one).  Touching its lines during the last K-blocks, or loading both rounds here, was no
+      // faster (463 and 457 us).
       v4i res[NIT];
       if (res16) {
 #pragma unroll
