@@ -309,6 +309,17 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
   // one broadcast LDS read.
   constexpr int NBT = C::BN / 128 > 0 ? C::BN / 128 : 1;
   __shared__ __attribute__((aligned(16))) float sws[NBT * 256];
+  // the tile's bias, staged with them (loaded in the epilogue: 401 against 398 us, 4096 x 28672 x 4096 silu)
+  __shared__ __attribute__((aligned(16))) float bias_lds[Args::kEpilogue ? C::BN : 4];
+  if constexpr (Args::kEpilogue) {
+    if (p.ep.bias != nullptr) {
+      for (int c = tid * 4; c < C::BN; c += C::THREADS * 4) {
+        float b[4];
+        load_values<4>(p.ep.bias, p.ep.bias_dtype, n0 + c, b);
+        *reinterpret_cast<v4f*>(bias_lds + c) = v4f{b[0], b[1], b[2], b[3]};
+      }
+    }
+  }
   if constexpr (SCH != 2) {
     for (int idx = tid; idx < NBT * KB; idx += C::THREADS) {
       const int b = idx / KB, k = idx - b * KB;
@@ -479,10 +490,9 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
       if (p.ep.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < C::TN; ++i) {
-          float b[4];
-          load_values<4>(p.ep.bias, p.ep.bias_dtype, n0 + wn * (C::BN / C::WN) + i * 16 + 4 * (lane >> 4), b);
+          const v4f b = *reinterpret_cast<const v4f*>(bias_lds + wn * (C::BN / C::WN) + i * 16 + 4 * (lane >> 4));
 #pragma unroll
-          for (int j = 0; j < C::TM; ++j) acc[i][j] += v4f{b[0], b[1], b[2], b[3]};
+          for (int j = 0; j < C::TM; ++j) acc[i][j] += b;
         }
       }
       with_activation(p.ep.act, [&](auto fn) {
@@ -515,7 +525,10 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
     const int ch = tid % CPR, mr0 = tid / CPR;
     const int64_t ncol = n0 + ch * 8;
     float bias[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.ep.bias != nullptr) load_values<8>(p.ep.bias, p.ep.bias_dtype, ncol, bias);
+    if (p.ep.bias != nullptr) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) bias[q] = bias_lds[ch * 8 + q];
+    }
     const bool res16 = p.ep.residual_dtype == 0, res32 = !res16;
     const int wrow = wm * (C::BM / C::WM);
 #pragma unroll
