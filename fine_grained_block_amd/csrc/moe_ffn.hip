@@ -65,6 +65,9 @@ struct Space {
   uint8_t* hq;
   float* hs;
   float* hf;           // [experts * T, I]: the product itself, where the down launch quantizes it
+  float* gu;           // [K slices][tiles * 16][2][I]: gate and up sums, where K is sliced
+  float* yp;           // [expert slices][T][H]: weighted sums, where the experts are sliced
+  int rows, kper;      // tiles * 16; K-blocks per slice
 };
 
 int max_experts(int T, int top_k, int E) { return T * top_k < E ? T * top_k : E; }
@@ -86,6 +89,36 @@ constexpr int kLateValues = 32 << 10, kLateBlocks = 62;
 bool late_quant(int T, int top_k, int E, int H, int I) {
   return T <= kTile && fused_prep(T, H) && max_experts(T, top_k, E) * T * (I / 128) <= kLateValues / 128 &&
          (I / 128 < 64 ? I / 128 : 64) * T <= kLateBlocks;
+}
+
+// Few experts or a narrow layer give few workgroups, and a CU's share of the stream is bounded (above):
+// then the launches are sliced over grid.z (gate+up, along K) and grid.y (down, over the experts'
+// K-blocks), with float32 partial sums added in slice order by one more launch each, which costs 3 to
+// 4 us: about 8 K-blocks of a gate+up workgroup's time.  Slices fill the 256 CUs and keep at least 4
+// K-blocks per wave.  Measured, tokens x experts x top_k x H x I, whole layer without and with slices:
+// 64 x 4 x 2 x 7168 x 2048 93 and 58 us, 64 x 2 x 1 x 7168 x 2048 86 and 43, 16 x 4 x 2 x 4096 x 1024 36.6
+// and 24.7 (gate+up); 32 x 32 x 4 x 512 x 4096 98 and 62, 8 x 64 x 6 x 2048 x 1408 65 and 58 (down).
+int gate_up_slices(int T, int top_k, int E, int H, int I) {
+  const int wgs = max_experts(T, top_k, E) * (I / 128), KB = H / 128;
+  if (wgs >= 128 || KB < 16) return 1;
+  int n = 256 / wgs;
+  if (n > KB / 4) n = KB / 4;
+  return n > 16 ? 16 : n;
+}
+bool down_wide(int H) { return H / 32 >= 160; }
+int down_slices(int T, int top_k, int E, int H, int I) {
+  const int wgs = H / (down_wide(H) ? 32 : 16), units = max_experts(T, top_k, E) * (I / 128);
+  if (wgs > 128 || units < 8 * 12) return 1;
+  int n = 256 / wgs;
+  if (n > units / (8 * 4)) n = units / (8 * 4);
+  return n > 16 ? 16 : n;
+}
+// Late quantization where its 64-column workgroups occupy the CUs, or slicing gains little (1 token, 64
+// experts, top 8, 2048 x 1024: 128 workgroups 22.2 us, 4 slices 24.0; 8 experts, top 2, 4096 x 512: 16
+// workgroups 20.8 us, 8 slices 16.2).
+bool use_late(int T, int top_k, int E, int H, int I) {
+  return late_quant(T, top_k, E, H, I) &&
+         (max_experts(T, top_k, E) * (I / 64) >= 96 || gate_up_slices(T, top_k, E, H, I) < 4);
 }
 
 // Tiles of 16 rows: with the prep launch they are packed (sum over experts of ceil(rows / 16) <=
@@ -111,10 +144,15 @@ size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
   t.row_weight = (float*)take(rows * sizeof(float));
   t.xq = take((size_t)T * H);
   t.xs = (float*)take((size_t)T * (H / 128) * sizeof(float));
-  const bool late = late_quant(T, top_k, E, H, I);
+  const bool late = use_late(T, top_k, E, H, I);
+  const int ks = late ? 1 : gate_up_slices(T, top_k, E, H, I), es = down_slices(T, top_k, E, H, I);
   t.hq = take(late ? 0 : rows * I);
   t.hs = (float*)take(late ? 0 : rows * (I / 128) * sizeof(float));
   t.hf = (float*)take(late ? (size_t)max_experts(T, top_k, E) * T * I * sizeof(float) : 0);
+  t.gu = (float*)take(ks > 1 ? ks * rows * 2 * I * sizeof(float) : 0);
+  t.yp = (float*)take(es > 1 ? (size_t)es * T * H * sizeof(float) : 0);
+  t.rows = (int)rows;
+  t.kper = (H / 128 + ks - 1) / ks;
   if (s) *s = t;
   return at;
 }
@@ -427,7 +465,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
   const int r = lane & 15, g = lane >> 4;
   int e, tile0, rows;
   if constexpr (FUSED) {
-    const Routed ex = find_expert(p, s, blockIdx.y, blockIdx.x == 0, sid, bits, tokens);
+    const Routed ex = find_expert(p, s, blockIdx.y, blockIdx.x == 0 && blockIdx.z == 0, sid, bits, tokens);
     if (ex.e < 0) return;
     e = ex.e;
     tile0 = ex.tile0;
@@ -445,7 +483,10 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
   tile0 = __builtin_amdgcn_readfirstlane(tile0);
   rows = __builtin_amdgcn_readfirstlane(rows);
   const int KB = p.H / 128, NB = p.I / 128, gb = blockIdx.x * COLS / 128;
-  const int ct = wave % CT, kbeg = wave / CT * ((KB + 1) / 2), kend = COLS == 64 && wave < CT ? (KB + 1) / 2 : KB;
+  // this wave's K-blocks: the workgroup's slice, or (64 columns) one half
+  const int ct = wave % CT;
+  const int kbeg = COLS == 64 ? wave / CT * ((KB + 1) / 2) : min((int)blockIdx.z * s.kper, KB);
+  const int kend = COLS == 64 ? (wave < CT ? (KB + 1) / 2 : KB) : min(kbeg + s.kper, KB);
   // this lane's weight bytes from the expert's first: 32-bit offsets (2 I H <= 2^31), the K-block is the
   // buffer load's scalar offset
   const uint32_t wrow = (uint32_t)((blockIdx.x * COLS + ct * 16 + (lane >> 3)) * p.H + 16 * (lane & 7));
@@ -460,7 +501,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     constexpr int MT = decltype(mt_c)::value;
     // weights: blocks past the end repeat the last one (their scale is 0)
     int4 wv[CH][2][2];
-    auto block = [&](int kk) { return COLS == 128 ? min(kk, KB - 1) : max(min(kbeg + kk, kend - 1), 0); };
+    auto block = [&](int kk) { return max(min(kbeg + kk, kend - 1), 0); };
     auto load = [&](int kk, int d) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) wv[d][i / 2][i % 2] = bload16<kLastReadAux>(wexp, woff[i], (uint32_t)block(kk) * 128);
@@ -482,8 +523,8 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     }
     auto fetch = [&](int k0) {
 #pragma unroll
-      for (int i = 0; i < NA; ++i) av[i] = bload16<0>(s.xq, aoff[i] + min(k0 + ak, KB - 1) * 128, 0);
-      sv = bload4(s.xs, soff + min(k0 + min(sk, CH - 1), KB - 1) * 4);
+      for (int i = 0; i < NA; ++i) av[i] = bload16<0>(s.xq, aoff[i] + block(k0 + ak) * 128, 0);
+      sv = bload4(s.xs, soff + block(k0 + min(sk, CH - 1)) * 4);
     };
     float* const xscale = reinterpret_cast<float*>(xrows + p.T * p.H);
     // this lane's rows (FUSED; rows past the count repeat the last one)
@@ -501,7 +542,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
         *reinterpret_cast<int4*>(&atiles[buf][(ak * MT + q / kTile) * kFrag + (ac & 1) * 1024 +
                                               ((ac >> 1) * 16 + ((q % kTile) ^ (ac + 8 * (ak & 1)))) * 16]) = av[i];
       }
-      if (sk < CH) ascale[buf][sk][sr] = k0 + sk < KB ? sv : 0.0f;
+      if (sk < CH) ascale[buf][sk][sr] = kbeg + k0 + sk < kend ? sv : 0.0f;
     };
     v4f acc[2][MT];
 #pragma unroll
@@ -562,9 +603,9 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
       sws[1][k] = load_sw<SWF>(p.s_w13, sw0 + (int64_t)NB * KB + k);
     }
     if constexpr (FUSED) {
-      const int chunks = p.H / 16;
+      const int c0 = COLS == 64 ? 0 : kbeg * 8, chunks = COLS == 64 ? p.H / 16 : (kend - kbeg) * 8;
       for (int i = tid; i < rows * chunks; i += 512) {
-        const int q = i / chunks, c = i - q * chunks;
+        const int q = i / chunks, c = c0 + i - q * chunks;
         float sc;
         const int4 codes = quant_chunk(p.x + (int64_t)tokens[q] * p.ldx, c, sc);
         *reinterpret_cast<int4*>(xrows + c / 8 * p.T * 128 + swz(q, c % 8)) = codes;
@@ -610,6 +651,19 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
       }
       return;
     }
+    if (gridDim.z > 1) {  // a K slice: the sums as they are
+      if (COLS == 128) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m * kTile + r < rows) {
+            float* const q = s.gu + (((int64_t)blockIdx.z * s.rows + (tile0 + m) * kTile + r) * 2) * p.I + gb * 128 + wave * 16 + 4 * g;
+            gstore<v4f>(q, acc[0][m]);
+            gstore<v4f>(q + p.I, acc[1][m]);
+          }
+        }
+      }
+      return;
+    }
     // the gated product of this wave's 16 columns (lane: row r, columns 4 g .. 4 g + 3) and the rows'
     // maxima over the workgroup's 128 columns
     v4f h[MT];
@@ -645,6 +699,62 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
   if (MTMAX == 1 || rows <= 16) run(std::integral_constant<int, 1>{});
   else if (MTMAX == 2 || rows <= 32) run(std::integral_constant<int, MTMAX < 2 ? 1 : 2>{});
   else run(std::integral_constant<int, MTMAX < 4 ? 1 : 4>{});
+}
+
+// The sliced gate+up sums: grid (I / 128, tiles), 16 threads per row of 16, 8 columns each.  Slices in
+// order, then activation, gate and quantization as above.
+__global__ __launch_bounds__(256) void moe_gate_up_finish_kernel(MoeArgs p, Space s, int slices) {
+  const int active = gload<int>(s.active);
+  if (active == 0) return;
+  const v4i last = gload<v4i>(s.experts + active - 1);
+  const int tile = blockIdx.y, row = threadIdx.x >> 4, j = threadIdx.x & 15, gb = blockIdx.x, NB = p.I / 128;
+  if (tile >= last[1] + (last[2] + kTile - 1) / kTile) return;
+  // (a tile's rows past its count were not written: their sums are dropped values in their own places)
+  const float* q = s.gu + ((int64_t)(tile * kTile + row) * 2) * p.I + gb * 128 + 8 * j;
+  float gate[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gate[i] = u[i] = 0.0f;
+  for (int z = 0; z < slices; ++z, q += (int64_t)s.rows * 2 * p.I) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const v4f a = gload<v4f>(q + 4 * i), b = gload<v4f>(q + p.I + 4 * i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        gate[4 * i + k] += a[k];
+        u[4 * i + k] += b[k];
+      }
+    }
+  }
+  activate<8>(p.act, gate);
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    gate[i] *= u[i];
+    mx = fmaxf(mx, fabsf(gate[i]));
+  }
+  const float sc = row16_max(mx) * kInvMax;
+  v2u c;
+  c[0] = codes4(gate[0], gate[1], gate[2], gate[3], sc);
+  c[1] = codes4(gate[4], gate[5], gate[6], gate[7], sc);
+  uint8_t* hq = s.hq + ((int64_t)tile * NB + gb) * kFrag;
+  gstore<v2u>(hq + (j >> 1 & 1) * 1024 + ((j >> 2) * 16 + row) * 16 + (j & 1) * 8, c);
+  if (j == 0) gstore<float>(s.hs + ((int64_t)tile * NB + gb) * kTile + row, sc);
+}
+
+// The sliced weighted sums: slices in order, the residual, one rounding.
+template <int OUT>
+__global__ __launch_bounds__(256) void moe_down_finish_kernel(MoeArgs p, Space s, int slices) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.T * (p.H / 4)) return;
+  const int t = i / (p.H / 4), n = (i - t * (p.H / 4)) * 4;
+  v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int z = 0; z < slices; ++z) sum += gload<v4f>(s.yp + ((int64_t)z * p.T + t) * p.H + n);
+  if (p.residual != nullptr) {
+    float f[4];
+    load_values<4>(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n, f);
+    sum += v4f{f[0], f[1], f[2], f[3]};
+  }
+  store4<OUT>(p.y, p.ldy, t, n, sum);
 }
 
 // Activations of the down products: the quantized product's fragments from the workspace ...
@@ -710,8 +820,8 @@ struct LateActs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// down: grid H / (16 NT), WK waves.  The K-blocks of all routed experts, in expert order, are one list
-// that the waves split evenly; a wave walks its share expert by expert (segments).
+// down: grid (H / (16 NT), slices), WK waves.  The K-blocks of all routed experts, in expert order, are
+// one list that the slices' waves split evenly; a wave walks its share expert by expert (segments).
 // ---------------------------------------------------------------------------------------------
 template <int SWF, int OUT, int MTMAX, int NT, int WK, bool LATE>
 __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
@@ -731,9 +841,9 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
   // used), later ones are loaded when they come up
   const v4i table = gload<v4i>(s.experts + min(lane, min(p.T * p.top_k, p.E) - 1));
   const int units = gload<int>(s.active) * KB;
-  const int per = (units + WK - 1) / WK;
-  int u = __builtin_amdgcn_readfirstlane(min(units, wave * per));
-  const int u1 = __builtin_amdgcn_readfirstlane(min(units, (wave + 1) * per));
+  const int part = blockIdx.y * WK + wave, per = (units + WK * (int)gridDim.y - 1) / (WK * (int)gridDim.y);
+  int u = __builtin_amdgcn_readfirstlane(min(units, part * per));
+  const int u1 = __builtin_amdgcn_readfirstlane(min(units, (part + 1) * per));
   while (u < u1) {
     const int si = u / KB, kb0 = u - si * KB;
     const int nk = min(min(KB - kb0, u1 - u), 64);
@@ -818,6 +928,10 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
     v4f sum = *reinterpret_cast<const v4f*>(ysum + t * COLS + c);
 #pragma unroll
     for (int q = 1; q < WK; ++q) sum += *reinterpret_cast<const v4f*>(ysum + (q * p.T + t) * COLS + c);
+    if (gridDim.y > 1) {  // a slice
+      gstore<v4f>(s.yp + ((int64_t)blockIdx.y * p.T + t) * p.H + n0 + c, sum);
+      continue;
+    }
     if (p.residual != nullptr) {
       float f[4];
       load_values<4>(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n0 + c, f);
@@ -836,8 +950,8 @@ size_t moe_ffn_workspace_bytes(int T, int top_k, int E, int H, int I) {
 namespace {
 
 template <int MTMAX, bool FUSED, int COLS>
-void launch_gate_up(const MoeArgs& a, const Space& s, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.I / COLS), (unsigned)max_experts(a.T, a.top_k, a.E)), block(512);
+void launch_gate_up(const MoeArgs& a, const Space& s, int slices, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.I / COLS), (unsigned)max_experts(a.T, a.top_k, a.E), (unsigned)slices), block(512);
   const size_t lds = FUSED ? (size_t)a.T * (a.H + a.H / 128 * sizeof(float)) : 0;
   if (a.s_w_fmt == 0) hipLaunchKernelGGL((moe_gate_up_kernel<0, MTMAX, FUSED, COLS>), grid, block, lds, stream, a, s);
   else hipLaunchKernelGGL((moe_gate_up_kernel<1, MTMAX, FUSED, COLS>), grid, block, lds, stream, a, s);
@@ -846,23 +960,32 @@ void launch_gate_up(const MoeArgs& a, const Space& s, hipStream_t stream) {
 template <int MTMAX>
 hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
   hipError_t e;
-  const bool late = late_quant(a.T, a.top_k, a.E, a.H, a.I);
+  const bool late = use_late(a.T, a.top_k, a.E, a.H, a.I);
+  // (no empty slice: kper blocks each)
+  const int ks = late ? 1 : (a.H / 128 + s.kper - 1) / s.kper;
+  const int es = down_slices(a.T, a.top_k, a.E, a.H, a.I);
   if (MTMAX == 1 && late) {
-    launch_gate_up<1, true, 64>(a, s, stream);
+    launch_gate_up<1, true, 64>(a, s, 1, stream);
   } else if (MTMAX * kTile <= kFusedTokens && fused_prep(a.T, a.H)) {
-    launch_gate_up<MTMAX * kTile <= kFusedTokens ? MTMAX : 1, true, 128>(a, s, stream);
+    launch_gate_up<MTMAX * kTile <= kFusedTokens ? MTMAX : 1, true, 128>(a, s, ks, stream);
   } else {
     hipLaunchKernelGGL(moe_prep_kernel, dim3((unsigned)a.T + 1), dim3(PREP), 0, stream, a, s);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    launch_gate_up<MTMAX, false, 128>(a, s, stream);
+    launch_gate_up<MTMAX, false, 128>(a, s, ks, stream);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (ks > 1) {
+    hipLaunchKernelGGL(moe_gate_up_finish_kernel, dim3((unsigned)(a.I / 128), (unsigned)(s.rows / kTile)), dim3(256), 0,
+                       stream, a, s, ks);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   // (late: one activation tile, T <= 16)
   const size_t extra = late ? (size_t)8 * (a.I / 128 < 64 ? a.I / 128 : 64) * a.T * 132 : 0;
 #define FGB_DOWN_LATE(SWF, OUT, NT, WK, LATE)                                                                     \
-  hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, LATE ? 1 : MTMAX, NT, WK, LATE>), dim3((unsigned)(a.H / (16 * NT))), \
+  hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, LATE ? 1 : MTMAX, NT, WK, LATE>), dim3((unsigned)(a.H / (16 * NT)), (unsigned)es), \
                      dim3(64 * WK), (size_t)WK * a.T * 16 * NT * sizeof(float) + extra, stream, a, s)
 #define FGB_DOWN(SWF, OUT, NT, WK)                            \
   do {                                                        \
@@ -883,11 +1006,16 @@ hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
   // where that would leave CUs without a workgroup (measured: H = 7168, 224 workgroups of 32 columns
   // 20.2 us against 448 of 16 23.6 at 1 token, 86 against 139 at 64; H = 2048, 128 workgroups of 16
   // columns 17.0 us against 64 of 32 24.5)
-  if (a.H / 32 >= 160) FGB_DOWN_TYPES(2, 8);
+  if (down_wide(a.H)) FGB_DOWN_TYPES(2, 8);
   else FGB_DOWN_TYPES(1, 8);
 #undef FGB_DOWN_TYPES
 #undef FGB_DOWN
 #undef FGB_DOWN_LATE
+  e = hipGetLastError();
+  if (e != hipSuccess || es == 1) return e;
+  const dim3 fgrid((unsigned)((a.T * (a.H / 4) + 255) / 256));
+  if (a.y_dtype == 0) hipLaunchKernelGGL(moe_down_finish_kernel<0>, fgrid, dim3(256), 0, stream, a, s, es);
+  else hipLaunchKernelGGL(moe_down_finish_kernel<1>, fgrid, dim3(256), 0, stream, a, s, es);
   return hipGetLastError();
 }
 

@@ -73,6 +73,8 @@ SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (1, 32, 8, 1024, 512), (2, 4
           (7, 32, 8, 1024, 256), (16, 8, 2, 512, 512), (17, 3, 1, 256, 256), (33, 5, 2, 640, 384), (64, 32, 8, 512, 256),
           (64, 64, 16, 256, 128), (49, 1, 1, 256, 512), (64, 300, 4, 128, 128), (5, 1024, 3, 128, 128),
           (9, 6, 3, 4096, 256), (20, 6, 3, 2048, 256), (4, 8, 8, 1024, 1152), (16, 8, 1, 128, 256), (3, 70, 24, 256, 128),
+          (40, 2, 1, 2048, 256), (16, 3, 2, 2048, 256), (24, 2, 2, 2432, 128), (1, 4, 1, 2048, 384),
+          (8, 16, 4, 256, 1024), (50, 12, 3, 128, 2048), (1, 16, 16, 256, 2048), (3, 40, 8, 2304, 1152),
           (2, 2, 1, 8320, 128), (2, 2, 2, 128, 9600), (1, 1, 1, 32768, 128), (1, 1, 1, 128, 32768)]
 
 
@@ -148,10 +150,11 @@ def test_zero_rows_and_zero_weights(dev):
     assert not y[1].any() and not y[2].any()
 
 
-def test_pitches_in_place_and_workspace_contents(dev):
+@pytest.mark.parametrize("T,E,k,H,I", [(21, 7, 3, 384, 256), (21, 12, 4, 256, 1280), (37, 3, 2, 2176, 256),
+                                       (1, 8, 8, 1024, 1024), (5, 8, 2, 4096, 256)])
+def test_pitches_in_place_and_workspace_contents(dev, T, E, k, H, I):
     """x, residual and out with row pitches above the row length, out = residual, a workspace that holds
     NaN patterns: equal, bit for bit, to the plain call, twice, and nothing outside out's rows is written."""
-    T, E, k, H, I = 21, 7, 3, 384, 256
     g = np.random.default_rng(6)
     res = torch.from_numpy(g.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).to(dev)
     y, x, ids, w, ops, dops = _run(dev, T, E, k, H, I, seed=6, residual=res)
