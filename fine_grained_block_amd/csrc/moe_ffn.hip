@@ -6,7 +6,7 @@
 //
 // What bounds it: every routed expert's 3 H I weight bytes are read once, and a token's share of
 // arithmetic on them is small, so the layer runs at the rate of the weight stream (HBM).  Three
-// launches, two for the fewest tokens:
+// launches, two for the fewest tokens, and one more each where gate+up or down is sliced:
 //   prep    quantizes the rows of x and, in one more workgroup, sorts the (token, expert) pairs by
 //           expert into tiles of 16 rows;
 //   gate+up a workgroup owns 128 columns of the intermediate of one expert: 8 waves, each streaming
@@ -17,8 +17,11 @@
 //           no prep launch;
 //   down    a workgroup owns 16 or 32 columns of y: its waves split the routed experts' K-blocks, add
 //           their weighted contributions per token in LDS in a fixed order, and the workgroup adds
-//           the waves' sums and the residual.  No partial sums in memory; the only atomics are the
-//           integer counters of the sort, whose order moves rows within a tile and changes no value.
+//           the waves' sums and the residual.
+// Where few experts or few columns would leave CUs idle, gate+up is sliced along K and down over the
+// experts' K-blocks; their float32 partial sums are then added in slice order by a launch of their own.
+// The only atomics are the integer counters of the sort, whose order moves rows within a tile and
+// changes no value.
 // The gated product's codes lie in the workspace in the matrix instruction's operand order: tile,
 // K-block, 16-byte half, lane (16 g + r holds bytes 32 g .. 32 g + 31 of row r), so a fragment is two
 // loads of whole lines.  Rows of a tile past its count are neither written nor read.  Weights are

@@ -19,9 +19,10 @@ from ._lib import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SCALE_TENSOR
 BLOCK = 128
 
 
-def _stream() -> int:
-    # the raw handle of the current stream (building a torch.cuda.Stream object costs microseconds)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _stream(device: int | None = None) -> int:
+    # the raw handle of the (given) current device's current stream: building a torch.cuda.Stream object
+    # costs microseconds
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -80,9 +81,9 @@ def _dense(t: torch.Tensor, name: str, dtypes, shape: tuple) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _on_device(*named) -> None:
+def _on_device(*named) -> int:
     """Every tensor lives on the current HIP device (checked after the shapes, so that shape
-    errors are reported without touching the device)."""
+    errors are reported without touching the device); returns the device."""
     cur = -1
     for name, t in named:
         if t is None:
@@ -96,6 +97,7 @@ def _on_device(*named) -> None:
             cur = torch.cuda.current_device()
         if at != cur:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    return cur
 
 
 def _blocks(n: int, what: str) -> int:
@@ -364,28 +366,39 @@ def gemm_epilogue(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: 
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {tuple(_ACTIVATIONS)}")
+    bias_ptr = res_ptr = None
+    bias_code = res_code = ldr = 0
+    given = [("a_q", a_q), ("s_a", s_a), ("w_q", w_q), ("s_w", s_w)]
     if bias is not None:
         _dense(bias, "bias", _VALUES, (N,))
+        bias_ptr, bias_code = bias.data_ptr(), _out_code(bias.dtype)
+        given.append(("bias", bias))
     if residual is not None:
         _need(isinstance(residual, torch.Tensor) and residual.dtype in _VALUES, "residual must be bf16 or float32")
         _matrix(residual, "residual", residual.dtype, rows=M, cols=N)
+        res_ptr, res_code, ldr = residual.data_ptr(), _out_code(residual.dtype), residual.stride(0)
+        given.append(("residual", residual))
     if workspace is not None:
         _need(workspace.is_contiguous(), "workspace must be contiguous")
-    _on_device(("a_q", a_q), ("s_a", s_a), ("w_q", w_q), ("s_w", s_w), ("bias", bias), ("residual", residual),
-               ("out", out), ("workspace", workspace))
+        given.append(("workspace", workspace))
+    if out is not None:
+        given.append(("out", out))
+    device = _on_device(*given)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
-    need = gemm_workspace_bytes(M, N, K)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().fgb_w8a8_block_gemm_epilogue(
-        _ptr(a_q), a_q.stride(0), _ptr(s_a), s_a.stride(0), _ptr(w_q), _ptr(s_w), _scale_fmt(s_w),
-        _ptr(bias), 0 if bias is None else _out_code(bias.dtype), act,
-        _ptr(residual), 0 if residual is None else _out_code(residual.dtype),
-        0 if residual is None else residual.stride(0), _ptr(out), _out_code(out.dtype), out.stride(0), M, N, K,
-        _ptr(workspace), ws_bytes, _stream())
-    check("fgb_w8a8_block_gemm_epilogue", st)
+    L = lib()
+    need = L.fgb_gemm_workspace_bytes(M, N, K)
+    ws_ptr, ws_bytes = None, 0
+    if need:
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = L.fgb_w8a8_block_gemm_epilogue(
+        a_q.data_ptr(), a_q.stride(0), s_a.data_ptr(), s_a.stride(0), w_q.data_ptr(), s_w.data_ptr(), _scale_fmt(s_w),
+        bias_ptr, bias_code, act, res_ptr, res_code, ldr, out.data_ptr(), _out_code(out.dtype), out.stride(0), M, N, K,
+        ws_ptr, ws_bytes, _stream(device))
+    if st:
+        check("fgb_w8a8_block_gemm_epilogue", st)
     return out
 
 
@@ -457,18 +470,19 @@ def moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", select
     if select_bias is not None:
         _dense(select_bias, "select_bias", (torch.float32,), (E,))
     if out is None:
-        _on_device(("logits", logits), ("select_bias", select_bias))
+        device = _on_device(("logits", logits), ("select_bias", select_bias))
         ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
         weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
     else:
         ids, weights = out
         _dense(ids, "ids", (torch.int32,), (T, top_k))
         _dense(weights, "weights", (torch.float32,), (T, top_k))
-        _on_device(("logits", logits), ("select_bias", select_bias), ("ids", ids), ("weights", weights))
-    st = lib().fgb_moe_route(_ptr(logits), _out_code(logits.dtype), logits.stride(0), T, E, top_k, score,
-                             _ptr(select_bias), int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights),
-                             _stream())
-    check("fgb_moe_route", st)
+        device = _on_device(("logits", logits), ("select_bias", select_bias), ("ids", ids), ("weights", weights))
+    st = lib().fgb_moe_route(logits.data_ptr(), _out_code(logits.dtype), logits.stride(0), T, E, top_k, score,
+                             _ptr(select_bias), bool(renormalize), scale, ids.data_ptr(), weights.data_ptr(),
+                             _stream(device))
+    if st:
+        check("fgb_moe_route", st)
     return ids, weights
 
 
@@ -485,9 +499,9 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_q: to
         y[t] = residual[t] + sum_j weights[t, j] * W2[e] . Q(act(W13[e, :I] . Q(x[t])) * (W13[e, I:] . Q(x[t])))
 
     with e = ids[t, j] (ids outside 0 .. E-1 are skipped) and Q the 1x128-group E4M3 quantization
-    (scales within an ulp of quantize()'s).  x bf16 [T, H]; ids int32 and weights float32 [T, top_k] (moe_route's result); w13_q
-    uint8 [E, 2I, H] (gate rows, then up rows) and w2_q uint8 [E, H, I] with their 128x128 block scales
-    (float32 or UE8M0, both alike); activation "silu", "gelu" or "gelu_tanh"; residual bf16 or
+    (scales within an ulp of quantize()'s).  x bf16 [T, H]; ids int32 and weights float32 [T, top_k]
+    (moe_route's result); w13_q uint8 [E, 2I, H] (gate rows, then up rows) and w2_q uint8 [E, H, I]
+    with their 128x128 block scales (float32 or UE8M0, both alike); activation "silu", "gelu" or "gelu_tanh"; residual bf16 or
     float32 [T, H], which may be `out` itself.  `workspace`: moe_ffn_workspace_bytes(T, top_k, E, H, I)
     bytes (allocated here when none is given).
     """
@@ -516,20 +530,22 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_q: to
         _matrix(out, "out", out.dtype, rows=T, cols=H)
     if workspace is not None:
         _need(workspace.is_contiguous(), "workspace must be contiguous")
-    _on_device(("x", x), ("ids", ids), ("weights", weights), ("w13_q", w13_q), ("s_w13", s_w13), ("w2_q", w2_q),
-               ("s_w2", s_w2), ("residual", residual), ("out", out), ("workspace", workspace))
+    device = _on_device(("x", x), ("ids", ids), ("weights", weights), ("w13_q", w13_q), ("s_w13", s_w13),
+                        ("w2_q", w2_q), ("s_w2", s_w2), ("residual", residual), ("out", out), ("workspace", workspace))
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype, device=x.device)
-    need = moe_ffn_workspace_bytes(T, top_k, E, H, I)
+    L = lib()
+    need = L.fgb_moe_ffn_workspace_bytes(T, top_k, E, H, I)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().fgb_moe_ffn(_ptr(x), x.stride(0), _ptr(ids), _ptr(weights), top_k, _ptr(w13_q), _ptr(s_w13), _ptr(w2_q),
-                           _ptr(s_w2), _scale_fmt(s_w13), E, act, _ptr(residual),
-                           0 if residual is None else _out_code(residual.dtype),
-                           0 if residual is None else residual.stride(0), _ptr(out), _out_code(out.dtype),
-                           out.stride(0), T, H, I, _ptr(workspace), ws_bytes, _stream())
-    check("fgb_moe_ffn", st)
+    st = L.fgb_moe_ffn(x.data_ptr(), x.stride(0), ids.data_ptr(), weights.data_ptr(), top_k, w13_q.data_ptr(),
+                       s_w13.data_ptr(), w2_q.data_ptr(), s_w2.data_ptr(), _scale_fmt(s_w13), E, act, _ptr(residual),
+                       0 if residual is None else _out_code(residual.dtype),
+                       0 if residual is None else residual.stride(0), out.data_ptr(), _out_code(out.dtype),
+                       out.stride(0), T, H, I, _ptr(workspace), ws_bytes, _stream(device))
+    if st:
+        check("fgb_moe_ffn", st)
     return out
 
 
