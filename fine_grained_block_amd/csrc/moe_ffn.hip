@@ -75,12 +75,17 @@ struct Space {
 
 int max_experts(int T, int top_k, int E) { return T * top_k < E ? T * top_k : E; }
 
-// Whether the gate+up workgroups find their expert and quantize its rows themselves (no prep launch):
-// the rows' codes, T * H bytes at most, have to leave LDS for two workgroups per CU.  Measured on 7168 x
-// 2048, 32 experts, top 8, without and with the prep launch (all launches): 1 token 70.7 and 73.8 us, 7
-// tokens (50 KB of codes, one workgroup per CU) 171 and 168 us.
-constexpr int kFusedTokens = 32, kFusedBytes = 32 << 10;
-bool fused_prep(int T, int H) { return T <= kFusedTokens && T * H <= kFusedBytes; }
+// Whether the gate+up workgroups find their expert and quantize its rows themselves (no prep launch).  Up
+// to 16 tokens the rows' codes, T * H bytes at most, have to leave LDS for two workgroups per CU; with more
+// the registers allow one only, and the limit is the time that quantizing takes.  Measured, tokens x
+// experts x top_k x H x I, all launches, without and with the prep launch: 1 x 32 x 8 x 7168 x 2048 70.7
+// and 73.8 us, 9 x 32 x 8 x 4096 x 2048 (36 KB) 131 and 138, 7 x 32 x 8 x 7168 x 2048 (49 KB, one workgroup
+// per CU) 171 and 168; 19 x 24 x 4 x 2048 x 1408 44.0 and 45.2, 32 x 8 x 2 x 2048 x 1024 (64 KB) 26.7 and
+// 27.9, 20 x 16 x 4 x 4096 x 1024 (80 KB) 58.1 and 56.1.
+constexpr int kFusedTokens = 32, kFusedBytes = 39 << 10, kFusedManyBytes = 64 << 10;
+bool fused_prep(int T, int H) {
+  return T <= kFusedTokens && T * H <= (T <= kTile ? kFusedBytes : kFusedManyBytes);
+}
 
 // Whether the gated product is quantized by the down launch.  A gate+up workgroup of 128 columns (the
 // quantization group) leaves half the CUs idle when one or two tokens reach only a few experts, and a CU
@@ -97,14 +102,18 @@ bool late_quant(int T, int top_k, int E, int H, int I) {
 // Few experts or a narrow layer give few workgroups, and a CU's share of the stream is bounded (above):
 // then the launches are sliced over grid.z (gate+up, along K) and grid.y (down, over the experts'
 // K-blocks), with float32 partial sums added in slice order by one more launch each, which costs 3 to
-// 4 us: about 8 K-blocks of a gate+up workgroup's time.  Slices fill the 256 CUs and keep at least 4
-// K-blocks per wave.  Measured, tokens x experts x top_k x H x I, whole layer without and with slices:
-// 64 x 4 x 2 x 7168 x 2048 93 and 58 us, 64 x 2 x 1 x 7168 x 2048 86 and 43, 16 x 4 x 2 x 4096 x 1024 36.6
-// and 24.7 (gate+up); 32 x 32 x 4 x 512 x 4096 98 and 62, 8 x 64 x 6 x 2048 x 1408 65 and 58 (down).
+// 4 us: about 8 K-blocks of a gate+up workgroup's time.  Slices fill the 256 CUs (more are slower, two of
+// each 16 x 8 x 2 x 7168 x 2048 67 us, four 74) and keep at least 4 K-blocks per wave.  Measured, tokens x
+// experts x top_k x H x I, whole layer without and with slices: 64 x 4 x 2 x 7168 x 2048 93 and 58 us, 64 x
+// 2 x 1 x 7168 x 2048 86 and 43, 16 x 4 x 2 x 4096 x 1024 36.6 and 24.7 (gate+up); 32 x 32 x 4 x 512 x 4096
+// 98 and 62, 8 x 64 x 6 x 2048 x 1408 65 and 58 (down).  From 128 to 255 gate+up workgroups two slices:
+// 16 x 8 x 2 x 7168 x 2048 80 and 67, 64 x 8 x 2 x 7168 x 2048 104 and 83, 24 x 8 x 2 x 4096 x 2048 55 and
+// 49, 64 x 16 x 4 x 2048 x 1024 45.5 and 43.6, but with short rows and two workgroups per CU (up to 16
+// tokens) 8 x 16 x 6 x 2048 x 1408 34.9 and 38.4.
 int gate_up_slices(int T, int top_k, int E, int H, int I) {
   const int wgs = max_experts(T, top_k, E) * (I / 128), KB = H / 128;
-  if (wgs >= 128 || KB < 16) return 1;
-  int n = 256 / wgs;
+  if (wgs >= 256 || KB < 16 || (wgs >= 128 && KB < 32 && T <= kTile)) return 1;
+  int n = wgs >= 128 ? 2 : 256 / wgs;
   if (n > KB / 4) n = KB / 4;
   return n > 16 ? 16 : n;
 }

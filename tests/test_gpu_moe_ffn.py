@@ -75,7 +75,9 @@ SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (1, 32, 8, 1024, 512), (2, 4
           (9, 6, 3, 4096, 256), (20, 6, 3, 2048, 256), (4, 8, 8, 1024, 1152), (16, 8, 1, 128, 256), (3, 70, 24, 256, 128),
           (40, 2, 1, 2048, 256), (16, 3, 2, 2048, 256), (24, 2, 2, 2432, 128), (1, 4, 1, 2048, 384),
           (8, 16, 4, 256, 1024), (50, 12, 3, 128, 2048), (1, 16, 16, 256, 2048), (3, 40, 8, 2304, 1152),
-          (2, 2, 1, 8320, 128), (2, 2, 2, 128, 9600), (1, 1, 1, 32768, 128), (1, 1, 1, 128, 32768)]
+          (2, 2, 1, 8320, 128), (2, 2, 2, 128, 9600), (1, 1, 1, 32768, 128), (1, 1, 1, 128, 32768),
+          (16, 6, 3, 2560, 384), (15, 32, 2, 2688, 512), (17, 32, 4, 2048, 512), (30, 3, 2, 2176, 256), (31, 3, 2, 2176, 256),
+          (12, 8, 3, 4096, 2048)]
 
 
 @pytest.mark.parametrize("T,E,k,H,I", SHAPES)
