@@ -385,13 +385,13 @@ def gemm_epilogue(a_q: torch.Tensor, s_a: torch.Tensor, w_q: torch.Tensor, s_w: 
         given.append(("out", out))
     device = _on_device(*given)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
+        out = a_q.new_empty((M, N), dtype=out_dtype)
     L = lib()
     need = L.fgb_gemm_workspace_bytes(M, N, K)
     ws_ptr, ws_bytes = None, 0
     if need:
         if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device)
+            workspace = a_q.new_empty(need)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = L.fgb_w8a8_block_gemm_epilogue(
         a_q.data_ptr(), a_q.stride(0), s_a.data_ptr(), s_a.stride(0), w_q.data_ptr(), s_w.data_ptr(), _scale_fmt(s_w),
@@ -471,8 +471,8 @@ def moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", select
         _dense(select_bias, "select_bias", (torch.float32,), (E,))
     if out is None:
         device = _on_device(("logits", logits), ("select_bias", select_bias))
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((T, top_k), dtype=torch.int32)
+        weights = logits.new_empty((T, top_k), dtype=torch.float32)
     else:
         ids, weights = out
         _dense(ids, "ids", (torch.int32,), (T, top_k))
@@ -533,11 +533,11 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_q: to
     device = _on_device(("x", x), ("ids", ids), ("weights", weights), ("w13_q", w13_q), ("s_w13", s_w13),
                         ("w2_q", w2_q), ("s_w2", s_w2), ("residual", residual), ("out", out), ("workspace", workspace))
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+        out = x.new_empty((T, H), dtype=out_dtype)
     L = lib()
     need = L.fgb_moe_ffn_workspace_bytes(T, top_k, E, H, I)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = L.fgb_moe_ffn(x.data_ptr(), x.stride(0), ids.data_ptr(), weights.data_ptr(), top_k, w13_q.data_ptr(),
                        s_w13.data_ptr(), w2_q.data_ptr(), s_w2.data_ptr(), _scale_fmt(s_w13), E, act, _ptr(residual),
