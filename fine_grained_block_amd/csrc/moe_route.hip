@@ -7,9 +7,11 @@
 //            selected: a row with fewer than k open experts fills up with id -1 and weight 0.
 //   weight   p_e, or p_e / (sum of the selected p) renormalized, times a scale.
 //
-// One wave per token, the row in registers (expert lane + 64 v in register v), so a row is read once
-// and nothing but the result is written: T * (E * 2 or 4 + 8 k) bytes.  Each selection is one wave-wide
-// integer maximum of order-preserving keys (four DPP steps and four lane reads) and a ballot.  The
+// One wave per token, or 16 lanes with many tokens, the row in registers (expert lane + 64 v in register
+// v), so a row is read once and nothing but the result is written: T * (E * 2 or 4 + 8 k) bytes.  Each
+// selection is one integer maximum of order-preserving keys over the token's lanes (four DPP steps, and four
+// lane reads for a wave) and a search for its lowest index: a few tokens are bound by that chain's
+// latency, many by its instructions.  The
 // renormalized weights are formed relative to the largest selected term, so they neither overflow
 // nor divide 0 by 0 however small the scores are.
 #include <type_traits>
@@ -23,18 +25,25 @@ namespace {
 
 constexpr int RT_WAVES = 4;  // tokens per workgroup
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  auto dpp = [](uint32_t x, auto ctrl) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, decltype(ctrl)::value, 0xF, 0xF, false);
+// f of v over each row of 16 lanes, for every lane of the row.
+template <typename T, typename F>
+__device__ __forceinline__ T row_reduce(T v, F f) {
+  auto dpp = [](T x, auto ctrl) {
+    return __builtin_bit_cast(
+        T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, false));
   };
-  // quad_perm [1,0,3,2], quad_perm [2,3,0,1], row_half_mirror, row_mirror: the maximum of 16 lanes
-  v = max(v, dpp(v, std::integral_constant<int, 0xB1>{}));
-  v = max(v, dpp(v, std::integral_constant<int, 0x4E>{}));
-  v = max(v, dpp(v, std::integral_constant<int, 0x141>{}));
-  v = max(v, dpp(v, std::integral_constant<int, 0x140>{}));
-  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
-  const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
-  return max(max(a, b), max(c, d));
+  // quad_perm [1,0,3,2], quad_perm [2,3,0,1], row_half_mirror, row_mirror
+  v = f(v, dpp(v, std::integral_constant<int, 0xB1>{}));
+  v = f(v, dpp(v, std::integral_constant<int, 0x4E>{}));
+  v = f(v, dpp(v, std::integral_constant<int, 0x141>{}));
+  return f(v, dpp(v, std::integral_constant<int, 0x140>{}));
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = row_reduce(v, umax);
+  auto row = [&](int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); };
+  return max(max(row(0), row(16)), max(row(32), row(48)));
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -57,24 +66,44 @@ __device__ __forceinline__ float sigmoid_exact(float l) {
   return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
+// Logit e of token t, for e >= E masked: NaN is masked (-inf); +inf counts as the largest finite value;
+// -0 and +0 are one value.  (Loads without branches, so that a row's are in flight together.)
+template <int DT>
+__device__ __forceinline__ float logit(const RouteArgs& p, int64_t t, int e) {
+  const float inf = __builtin_inff(), big = 3.4028234663852886e38f;
+  const int64_t at = t * p.ld + min(e, p.E - 1);
+  float x;
+  if constexpr (DT == 0) x = bf16_lo(gload<uint16_t>((const uint16_t*)p.logits + at));
+  else x = gload<float>((const float*)p.logits + at);
+  return e < p.E && x > -inf ? fminf(x, big) + 0.0f : -inf;
+}
+
+// Weight of a lane's selection (0 without one).  mx and sum reduce over a token's lanes, all of which come here.
+template <typename Max, typename Sum>
+__device__ __forceinline__ float selected_weight(const RouteArgs& p, bool have, float l, float row_max, float row_sum,
+                                                 Max mx, Sum sum) {
+  if (!p.renorm) return !have ? 0.0f : (p.scoring == 0 ? expf(l - row_max) / row_sum : sigmoid_exact(l));
+  const uint32_t m = mx(have ? order_key(l) : 0u);
+  const float top = order_value(m);
+  float w = 0.0f;
+  if (have) {
+    if (p.scoring == 0) w = expf(l - top);
+    else if (top >= 0.0f) w = sigmoid_exact(l);
+    else w = expf(l - top) / (1.0f + expf(l));  // every score times exp(-top)
+  }
+  const float s = sum(w);
+  return m != 0 ? w / s : 0.0f;
+}
+
 template <int V, int DT>
 __global__ __launch_bounds__(64 * RT_WAVES) void moe_route_kernel(RouteArgs p) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * RT_WAVES + (threadIdx.x >> 6);
   if (t >= p.T) return;
-  const float inf = __builtin_inff(), big = 3.4028234663852886e38f;
+  const float inf = __builtin_inff();
   float l[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane + 64 * v;
-    float x = -inf;
-    if (e < p.E) {
-      if constexpr (DT == 0) x = bf16_lo(gload<uint16_t>((const uint16_t*)p.logits + t * p.ld + e));
-      else x = gload<float>((const float*)p.logits + t * p.ld + e);
-    }
-    // NaN is masked; +inf counts as the largest finite value; -0 and +0 are one value
-    l[v] = x > -inf ? fminf(x, big) + 0.0f : -inf;
-  }
+  for (int v = 0; v < V; ++v) l[v] = logit<DT>(p, t, lane + 64 * v);
   // softmax: the row's maximum and sum (of the open experts)
   float row_max = 0.0f, row_sum = 1.0f;
   if (p.scoring == 0 && (p.bias != nullptr || !p.renorm)) {
@@ -93,8 +122,7 @@ __global__ __launch_bounds__(64 * RT_WAVES) void moe_route_kernel(RouteArgs p) {
   for (int v = 0; v < V; ++v) {
     float f = l[v];
     if (p.bias != nullptr) {
-      const int e = lane + 64 * v;
-      const float b = e < p.E ? gload<float>(p.bias + e) : 0.0f;
+      const float b = gload<float>(p.bias + min(lane + 64 * v, p.E - 1));
       f = (p.scoring == 0 ? expf(f - row_max) / row_sum : sigmoid_exact(f)) + b + 0.0f;
     }
     key[v] = l[v] > -inf ? order_key(f) : 0u;
@@ -132,29 +160,93 @@ __global__ __launch_bounds__(64 * RT_WAVES) void moe_route_kernel(RouteArgs p) {
         if (v == bv) key[v] = 0;
     }
   }
-  // weights of the selected (lanes without one: 0)
   const bool have = my_id >= 0;
-  float w = 0.0f;
-  if (p.renorm) {
-    const uint32_t m = wave_max_u32(have ? order_key(my_l) : 0u);
-    if (m != 0) {
-      const float top = order_value(m);
-      if (p.scoring == 0) {
-        w = have ? expf(my_l - top) : 0.0f;
-      } else if (top >= 0.0f) {
-        w = have ? sigmoid_exact(my_l) : 0.0f;
-      } else {  // every score times exp(-top): exp(l - top) / (1 + exp(l))
-        w = have ? expf(my_l - top) / (1.0f + expf(my_l)) : 0.0f;
-      }
-      w = w / wave_sum(w);
-    }
-  } else if (have) {
-    w = p.scoring == 0 ? expf(my_l - row_max) / row_sum : sigmoid_exact(my_l);
-  }
+  const float w = selected_weight(p, have, my_l, row_max, row_sum, wave_max_u32, wave_sum);
   if (lane < p.top_k) {
     gstore<int>(p.ids + t * p.top_k + lane, my_id);
     gstore<float>(p.weights + t * p.top_k + lane, have ? w * p.scale : 0.0f);
   }
+}
+
+// The same for many tokens: four tokens per wave, 16 lanes each (expert sub + 16 v in register v of the
+// row's lane sub), so that a selection's instructions serve four tokens.  The sums are added in the wave
+// kernel's order: a token's result is the same, bit for bit, whichever kernel computes it.
+template <int V, int DT>
+__global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs p) {
+  const int sub = threadIdx.x & 15;
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t t = row < p.T ? row : p.T - 1;  // (all lanes stay for the row reductions)
+  const float inf = __builtin_inff();
+  auto fadd = [](float a, float b) { return a + b; };
+  float l[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = logit<DT>(p, t, sub + 16 * v);
+  float row_max = 0.0f, row_sum = 1.0f;
+  if (p.scoring == 0 && (p.bias != nullptr || !p.renorm)) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = max(m, l[v] > -inf ? order_key(l[v]) : 0u);
+    m = row_reduce(m, umax);
+    row_max = m ? order_value(m) : 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v & 3] += l[v] > -inf ? expf(l[v] - row_max) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = row_reduce(s[i], fadd);
+    row_sum = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float f = l[v];
+    if (p.bias != nullptr) {
+      const float b = gload<float>(p.bias + min(sub + 16 * v, p.E - 1));
+      f = (p.scoring == 0 ? expf(f - row_max) / row_sum : sigmoid_exact(f)) + b + 0.0f;
+    }
+    key[v] = l[v] > -inf ? order_key(f) : 0u;
+  }
+  // lane j of the row keeps the j-th selection
+  int my_id = -1;
+  float my_l = -inf;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    const uint32_t m = row_reduce(best, umax);
+    if (__ballot(m != 0) == 0) break;
+    // this lane's lowest register that holds it, then the row's lowest index
+    uint32_t at = V;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) at = key[v] == m ? v : at;
+    const uint32_t mine = at < V ? 16 * at + sub : 0xFFFFu;
+    const uint32_t win = row_reduce(mine, [](uint32_t a, uint32_t b) { return min(a, b); });
+    if (sub == j && m != 0) { my_id = (int)win; my_l = order_value(m); }
+    const uint32_t gone = mine == win ? at : V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = gone == v ? 0u : key[v];
+  }
+  const bool have = my_id >= 0;
+  if (p.bias != nullptr && have) my_l = logit<DT>(p, t, my_id);  // (the keys held the biased score)
+  const float w = selected_weight(p, have, my_l, row_max, row_sum, [](uint32_t v) { return row_reduce(v, umax); },
+                                  [&](float v) { return row_reduce(v, fadd); });
+  if (row < p.T && sub < p.top_k) {
+    gstore<int>(p.ids + t * p.top_k + sub, my_id);
+    gstore<float>(p.weights + t * p.top_k + sub, have ? w * p.scale : 0.0f);
+  }
+}
+
+// From these many tokens on the waves of one token each are bound by instruction issue and four tokens per
+// wave win; below, each selection's chain of 16 registers a lane is the longer one.  Measured at 8
+// of 256 experts (one token a wave, four): 1 token 3.7 and 4.8 us, 4096 5.8 and 5.2, 8191 8.6 and 6.4, 16384
+// 14.2 and 9.5; with a selection bias 4096 6.6 and 7.3, 8191 10.1 and 8.6; 6 of 64 experts 4096 4.0 and 3.3,
+// 16384 8.8 and 4.6.
+constexpr int kManyTokens = 4096, kManyTokensBias = 6144;
+
+template <int V>
+void launch_rows(const RouteArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.T + 15) / 16)), block(256);
+  if (a.dtype == 0) hipLaunchKernelGGL((moe_route_rows_kernel<V, 0>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((moe_route_rows_kernel<V, 1>), grid, block, 0, stream, a);
 }
 
 template <int V>
@@ -167,6 +259,12 @@ void launch_v(const RouteArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
+  if (a.T >= (a.bias == nullptr ? kManyTokens : kManyTokensBias) && a.E <= 256 && a.top_k <= 16) {
+    if (a.E <= 64) launch_rows<4>(a, stream);
+    else if (a.E <= 128) launch_rows<8>(a, stream);
+    else launch_rows<16>(a, stream);
+    return hipGetLastError();
+  }
   // registers per lane: the next power of two of ceil(E / 64)
   if (a.E <= 64) launch_v<1>(a, stream);
   else if (a.E <= 128) launch_v<2>(a, stream);

@@ -120,3 +120,32 @@ def test_empty_and_many_rows(dev):
     ids, w = fgb.moe_route(l.to(dev), 2, scoring="sigmoid")
     pick = np.r_[0:300, 69000:70001]
     _check(ids[torch.from_numpy(pick).to(dev)], w[torch.from_numpy(pick).to(dev)], l[pick], 2, scoring="sigmoid")
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (7, 7), (16, 16), (17, 4), (64, 6), (65, 16), (128, 8), (130, 1), (255, 11),
+                                 (256, 8), (256, 16), (256, 17)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens_equal_few(dev, E, k, dtype):
+    """Thousands of tokens in one call: rows equal, bit for bit, to those of calls of fewer tokens (the sums'
+    order is the same), and to the oracle; odd counts, masked and empty rows, ties, a row pitch, garbage in the
+    outputs."""
+    T = 6157
+    l = _logits(T, E, 7, dtype, 0.3)
+    l[5::97] = -float("inf")
+    l[11::89] = 0.5
+    l[13::83] = float("nan")
+    buf = torch.full((T, E + 3), 9.0, dtype=dtype, device=dev)
+    buf[:, :E] = l.to(dev)
+    d = buf[:, :E]
+    bias = torch.from_numpy(np.random.default_rng(8).standard_normal(E).astype(np.float32)).to(dev)
+    pick = np.r_[0:40, 3000:3040, T - 40:T]
+    for scoring in ("softmax", "sigmoid"):
+        for renorm, b in ((True, None), (False, None), (True, bias), (False, bias)):
+            out = (torch.full((T, k), 77, dtype=torch.int32, device=dev), torch.full((T, k), float("nan"), device=dev))
+            fgb.moe_route(d, k, scoring=scoring, select_bias=b, renormalize=renorm, out=out)
+            for a in range(0, T, 2053):
+                ids, w = fgb.moe_route(d[a:a + 2053], k, scoring=scoring, select_bias=b, renormalize=renorm)
+                assert torch.equal(out[0][a:a + 2053], ids) and torch.equal(out[1][a:a + 2053], w)
+            if b is None:
+                at = torch.from_numpy(pick).to(dev)
+                _check(out[0][at], out[1][at], l[pick], k, scoring=scoring, renormalize=renorm)
