@@ -12,7 +12,8 @@
 //   gelu_tanh  v/2 * (1 + tanh u) = v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
 //   silu       v * sigmoid(v)
 // sigmoid(z) = 1 / (1 + exp(-z)): for z -> -inf the exponential is +inf and the quotient 0, so no
-// form overflows into a NaN.
+// finite v overflows into a NaN.  A NaN stays one in every form, +inf stays +inf, and -inf gives what the
+// formulas do: 0 for relu, NaN (-inf * 0) for the others.
 #pragma once
 #include "gemm_common.hpp"
 #include "internal.h"
@@ -31,7 +32,8 @@ __device__ __forceinline__ float gelu_erf(float v) {
   q = __builtin_fmaf(q, t, 0.0973725319f);
   q = __builtin_fmaf(q, t, 0.119791359f);
   q = __builtin_fmaf(q, t, 0.118412219f);
-  const float h = v * (q * t * __builtin_amdgcn_exp2f(v * v * -0.72134752f));
+  // (min: v h is 0 long before 16 in the upper tail, and at +inf it would be inf * 0)
+  const float h = fminf(v, 16.0f) * (q * t * __builtin_amdgcn_exp2f(v * v * -0.72134752f));
   return v < 0.0f ? h : v - h;
 }
 
@@ -46,7 +48,7 @@ __device__ __forceinline__ void with_activation(int act, F f) {
   if (act == kActSilu) f([](float v) { return v * sigmoidf(v); });
   else if (act == kActGeluTanh) f([](float v) { return gelu_tanh(v); });
   else if (act == kActGelu) f([](float v) { return gelu_erf(v); });
-  else if (act == kActRelu) f([](float v) { return fmaxf(v, 0.0f); });
+  else if (act == kActRelu) f([](float v) { return v < 0.0f ? 0.0f : v; });  // (a maximum would turn NaN into 0)
 }
 template <int W>
 __device__ __forceinline__ void activate(int act, float (&v)[W]) {
