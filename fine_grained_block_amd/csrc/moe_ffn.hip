@@ -32,13 +32,13 @@
 #include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "internal.h"
+#include "moe_plan.hpp"
 #include "quant_common.hpp"
 
 namespace fgb {
 
 namespace {
 
-constexpr int kTile = 16;           // rows per activation tile
 constexpr int kFrag = kTile * 128;  // bytes of a tile's K-block
 
 // 16-byte chunk c of 128-byte row r at c ^ ((r & 7) ^ (r>>3 & 1)): conflict-free 16-row fragment reads.
@@ -72,74 +72,6 @@ struct Space {
   float* yp;           // [expert slices][T][H]: weighted sums, where the experts are sliced
   int rows, kper;      // tiles * 16; K-blocks per slice
 };
-
-int max_experts(int T, int top_k, int E) { return T * top_k < E ? T * top_k : E; }
-
-// Whether the gate+up workgroups find their expert and quantize its rows themselves (no prep launch).  Up
-// to 16 tokens the rows' codes, T * H bytes at most, have to leave LDS for two workgroups per CU; with more
-// the registers allow one only, and the limit is the time that quantizing takes.  Measured, tokens x
-// experts x top_k x H x I, all launches, without and with the prep launch: 1 x 32 x 8 x 7168 x 2048 70.7
-// and 73.8 us, 9 x 32 x 8 x 4096 x 2048 (36 KB) 131 and 138, 7 x 32 x 8 x 7168 x 2048 (49 KB, one workgroup
-// per CU) 171 and 168; 19 x 24 x 4 x 2048 x 1408 44.0 and 45.2, 32 x 8 x 2 x 2048 x 1024 (64 KB) 26.7 and
-// 27.9, 20 x 16 x 4 x 4096 x 1024 (80 KB) 58.1 and 56.1.
-constexpr int kFusedTokens = 32, kFusedBytes = 39 << 10, kFusedManyBytes = 64 << 10;
-bool fused_prep(int T, int H) {
-  return T <= kFusedTokens && T * H <= (T <= kTile ? kFusedBytes : kFusedManyBytes);
-}
-
-// Whether the gated product is quantized by the down launch.  A gate+up workgroup of 128 columns (the
-// quantization group) leaves half the CUs idle when one or two tokens reach only a few experts, and a CU
-// takes in no more than about 16 bytes a clock whatever is in flight (128 workgroups: 5.0 TB/s with 3
-// or with 7 K-blocks ahead); workgroups of 64 columns write the float32 product and every down
-// workgroup quantizes all of it, which has to stay small.  Measured at 1 token (7168 x 2048, 32 experts,
-// top 8): gate+up 50.2 -> 40.5 us, down 20.5 -> 22.4 us.
-constexpr int kLateValues = 32 << 10, kLateBlocks = 62;
-bool late_quant(int T, int top_k, int E, int H, int I) {
-  return T <= kTile && fused_prep(T, H) && max_experts(T, top_k, E) * T * (I / 128) <= kLateValues / 128 &&
-         (I / 128 < 64 ? I / 128 : 64) * T <= kLateBlocks;
-}
-
-// Few experts or a narrow layer give few workgroups, and a CU's share of the stream is bounded (above):
-// then the launches are sliced over grid.z (gate+up, along K) and grid.y (down, over the experts'
-// K-blocks), with float32 partial sums added in slice order by one more launch each, which costs 3 to
-// 4 us: about 8 K-blocks of a gate+up workgroup's time.  Slices fill the 256 CUs (more are slower, two of
-// each 16 x 8 x 2 x 7168 x 2048 67 us, four 74) and keep at least 4 K-blocks per wave.  Measured, tokens x
-// experts x top_k x H x I, whole layer without and with slices: 64 x 4 x 2 x 7168 x 2048 93 and 58 us, 64 x
-// 2 x 1 x 7168 x 2048 86 and 43, 16 x 4 x 2 x 4096 x 1024 36.6 and 24.7 (gate+up); 32 x 32 x 4 x 512 x 4096
-// 98 and 62, 8 x 64 x 6 x 2048 x 1408 65 and 58 (down).  From 128 to 255 gate+up workgroups two slices:
-// 16 x 8 x 2 x 7168 x 2048 80 and 67, 64 x 8 x 2 x 7168 x 2048 104 and 83, 24 x 8 x 2 x 4096 x 2048 55 and
-// 49, 64 x 16 x 4 x 2048 x 1024 45.5 and 43.6, but with short rows and two workgroups per CU (up to 16
-// tokens) 8 x 16 x 6 x 2048 x 1408 34.9 and 38.4.
-int gate_up_slices(int T, int top_k, int E, int H, int I) {
-  const int wgs = max_experts(T, top_k, E) * (I / 128), KB = H / 128;
-  if (wgs >= 256 || KB < 16 || (wgs >= 128 && KB < 32 && T <= kTile)) return 1;
-  int n = wgs >= 128 ? 2 : 256 / wgs;
-  if (n > KB / 4) n = KB / 4;
-  return n > 16 ? 16 : n;
-}
-bool down_wide(int H) { return H / 32 >= 160; }
-int down_slices(int T, int top_k, int E, int H, int I) {
-  const int wgs = H / (down_wide(H) ? 32 : 16), units = max_experts(T, top_k, E) * (I / 128);
-  if (wgs > 128 || units < 8 * 12) return 1;
-  int n = 256 / wgs;
-  if (n > units / (8 * 4)) n = units / (8 * 4);
-  return n > 16 ? 16 : n;
-}
-// Late quantization where its 64-column workgroups occupy the CUs, or slicing gains little (1 token, 64
-// experts, top 8, 2048 x 1024: 128 workgroups 22.2 us, 4 slices 24.0; 8 experts, top 2, 4096 x 512: 16
-// workgroups 20.8 us, 8 slices 16.2).
-bool use_late(int T, int top_k, int E, int H, int I) {
-  return late_quant(T, top_k, E, H, I) &&
-         (max_experts(T, top_k, E) * (I / 64) >= 96 || gate_up_slices(T, top_k, E, H, I) < 4);
-}
-
-// Tiles of 16 rows: with the prep launch they are packed (sum over experts of ceil(rows / 16) <=
-// (pairs + 15 experts) / 16), without it every routed expert has room for all tokens.
-int expert_tiles(int T) { return (T + kTile - 1) / kTile; }
-int max_tiles(int T, int top_k, int E, int H) {
-  const int n = max_experts(T, top_k, E);
-  return fused_prep(T, H) ? n * expert_tiles(T) : T * top_k / kTile + n;
-}
 
 size_t layout(int T, int top_k, int E, int H, int I, uint8_t* base, Space* s) {
   const size_t tiles = (size_t)max_tiles(T, top_k, E, H), rows = tiles * kTile;
@@ -839,7 +771,7 @@ template <int SWF, int OUT, int MTMAX, int NT, int WK, bool LATE>
 __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
   constexpr int COLS = 16 * NT;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WK][NT * kFrag];
-  // [WK waves][T][COLS]; LATE: then each wave's codes and scales of a segment
+  // [WK waves][T][COLS]; LATE: then the waves' codes and scales of a segment (late_codes_at, late_scales_at)
   extern __shared__ __attribute__((aligned(16))) float ysum[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -880,16 +812,17 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
       constexpr int D = 3;  // blocks in registers (4: 2-8% slower with one row tile, registers; 2: 5% with four)
       std::conditional_t<LATE, LateActs, StoredActs<MT, D>> acts;
       if constexpr (LATE) {
-        const int seg = min(KB, 64);
-        uint8_t* const mem = reinterpret_cast<uint8_t*>(ysum + WK * p.T * COLS) + wave * seg * p.T * 132;
+        static_assert(WK == kDownWaves, "LDS layout");
+        const int seg = late_segment(p.I);
+        uint8_t* const mem = reinterpret_cast<uint8_t*>(ysum + WK * p.T * COLS);
         acts.h = s.hf + (int64_t)si * p.T * p.I + kb0 * 128;
         acts.pitch = p.I;
         acts.T = p.T;
         acts.rows = rows;
         acts.nk = nk;
         acts.q = min(r, rows - 1);
-        acts.codes_lds = mem;
-        acts.scale_lds = reinterpret_cast<float*>(mem + seg * p.T * 128);
+        acts.codes_lds = mem + late_codes_at(wave, seg, p.T);
+        acts.scale_lds = reinterpret_cast<float*>(mem + late_scales_at(wave, seg, p.T));
       } else {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -995,7 +928,7 @@ hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   // (late: one activation tile, T <= 16)
-  const size_t extra = late ? (size_t)8 * (a.I / 128 < 64 ? a.I / 128 : 64) * a.T * 132 : 0;
+  const size_t extra = late ? (size_t)late_bytes(late_segment(a.I), a.T) : 0;
 #define FGB_DOWN_LATE(SWF, OUT, NT, WK, LATE)                                                                     \
   hipLaunchKernelGGL((moe_down_kernel<SWF, OUT, LATE ? 1 : MTMAX, NT, WK, LATE>), dim3((unsigned)(a.H / (16 * NT)), (unsigned)es), \
                      dim3(64 * WK), (size_t)WK * a.T * 16 * NT * sizeof(float) + extra, stream, a, s)
@@ -1018,8 +951,8 @@ hipError_t launch_layer(const MoeArgs& a, const Space& s, hipStream_t stream) {
   // where that would leave CUs without a workgroup (measured: H = 7168, 224 workgroups of 32 columns
   // 20.2 us against 448 of 16 23.6 at 1 token, 86 against 139 at 64; H = 2048, 128 workgroups of 16
   // columns 17.0 us against 64 of 32 24.5)
-  if (down_wide(a.H)) FGB_DOWN_TYPES(2, 8);
-  else FGB_DOWN_TYPES(1, 8);
+  if (down_wide(a.H)) FGB_DOWN_TYPES(2, kDownWaves);
+  else FGB_DOWN_TYPES(1, kDownWaves);
 #undef FGB_DOWN_TYPES
 #undef FGB_DOWN
 #undef FGB_DOWN_LATE
