@@ -55,6 +55,23 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return cvt_pk_e4m3<true>(c / v, d / v, cvt_pk_e4m3<false>(a / v, b / v, 0u));
 }
 
+// Group maxima are taken over magnitudes as bit patterns: finite values order like them and NaN lies above
+// all, so a NaN makes its group's scale NaN and reaches the output (a float maximum would drop it, and the
+// conversion to codes would make it finite).
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float group_scale(uint32_t m) { return __uint_as_float(m) * kInvMax; }
+// Maximum over 8 or 16 consecutive lanes, for all of them (quad_perm [1,0,3,2], quad_perm [2,3,0,1],
+// row_half_mirror, row_mirror).
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  static_assert(L == 8 || L == 16, "half a DPP row or a whole one");
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));
+  if constexpr (L == 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
+  return v;
+}
+
 // Workspace: the routed experts, each with its first tile and its row count; the tiles' rows (token
 // and weight); codes [T, H] and scales [T, H/128] of x; the gated product's codes and scales, the
 // scales [tile][K-block][16 rows].
@@ -115,7 +132,12 @@ static_assert(kMoeMaxPairs <= PREP && kMoeMaxExperts <= PREP, "one pair and one 
 __device__ __forceinline__ int4 quant_chunk(const uint16_t* x, int c, float& sc) {
   const int4 a = gload_i4(x + 16 * c), b = gload_i4(x + 16 * c + 8);
   const uint4 u = make_uint4(a.x, a.y, a.z, a.w), v = make_uint4(b.x, b.y, b.z, b.w);
-  sc = row8_max(fmaxf(absmax8(u), absmax8(v))) * kInvMax;
+  const uint32_t words[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+  v2us m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2us, words[i] & 0x7FFF7FFFu));
+  sc = group_scale(lanes_max<8>((uint32_t)max(m[0], m[1]) << 16));
   int4 q;
   q.x = codes4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y), sc);
   q.y = codes4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w), sc);
@@ -398,7 +420,7 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
   __shared__ __attribute__((aligned(1024))) uint8_t atiles[2][FUSED ? 16 : CH * MTMAX * kFrag];
   __shared__ float ascale[2][CH][FUSED ? 1 : MTMAX * kTile];
   __shared__ float sws[2][256];  // the two weight block rows' scales (H <= 32768)
-  __shared__ float amax[8][MTMAX * kTile];
+  __shared__ uint32_t amax[8][MTMAX * kTile];  // magnitudes
   // FUSED: the expert's rows, codes [H/128][T][128] (16-byte chunks swizzled by row) and scales [H/128][T]
   extern __shared__ __attribute__((aligned(1024))) uint8_t xrows[];
   __shared__ int sid[FUSED ? kMoeMaxPairs : 1];
@@ -615,24 +637,24 @@ __global__ __launch_bounds__(512, 2) void moe_gate_up_kernel(MoeArgs p, Space s)
     for (int m = 0; m < MT; ++m) {
       float v[4] = {acc[0][m][0], acc[0][m][1], acc[0][m][2], acc[0][m][3]};
       activate<4>(p.act, v);
-      float mx = 0.0f;
+      uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         h[m][i] = v[i] * acc[1][m][i];
-        mx = fmaxf(mx, fabsf(h[m][i]));
+        mx = max(mx, magnitude(h[m][i]));
       }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
       if (g == 0) amax[wave][m * kTile + r] = mx;
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * kTile + r < rows) {
-        float mx = amax[0][m * kTile + r];
+        uint32_t mx = amax[0][m * kTile + r];
 #pragma unroll
-        for (int q = 1; q < 8; ++q) mx = fmaxf(mx, amax[q][m * kTile + r]);
-        const float sc = mx * kInvMax;
+        for (int q = 1; q < 8; ++q) mx = max(mx, amax[q][m * kTile + r]);
+        const float sc = group_scale(mx);
         const uint32_t c = codes4(h[m][0], h[m][1], h[m][2], h[m][3], sc);
         uint8_t* hq = s.hq + ((int64_t)(tile0 + m) * NB + gb) * kFrag;
         gstore<uint32_t>(hq + (wave & 1) * 1024 + ((wave >> 1) * 16 + r) * 16 + 4 * g, c);
@@ -670,13 +692,13 @@ __global__ __launch_bounds__(256) void moe_gate_up_finish_kernel(MoeArgs p, Spac
     }
   }
   activate<8>(p.act, gate);
-  float mx = 0.0f;
+  uint32_t mx = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     gate[i] *= u[i];
-    mx = fmaxf(mx, fabsf(gate[i]));
+    mx = max(mx, magnitude(gate[i]));
   }
-  const float sc = row16_max(mx) * kInvMax;
+  const float sc = group_scale(lanes_max<16>(mx));
   v2u c;
   c[0] = codes4(gate[0], gate[1], gate[2], gate[3], sc);
   c[1] = codes4(gate[4], gate[5], gate[6], gate[7], sc);
@@ -735,17 +757,18 @@ struct LateActs {
     for (int i = lane >> 3; i < nk * rows; i += 8) {  // (whole 8-lane groups)
       const int kk = i / rows, row = i - kk * rows;
       const float* src = h + row * pitch + kk * 128 + 16 * (lane & 7);
-      float v[16], mx = 0.0f;
+      float v[16];
+      uint32_t mx = 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const v4f t = gload<v4f>(src + 4 * u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[4 * u + j] = t[j];
-          mx = fmaxf(mx, fabsf(t[j]));
+          mx = max(mx, magnitude(t[j]));
         }
       }
-      const float sc = row8_max(mx) * kInvMax;
+      const float sc = group_scale(lanes_max<8>(mx));
       int4 c;
       c.x = codes4(v[0], v[1], v[2], v[3], sc);
       c.y = codes4(v[4], v[5], v[6], v[7], sc);

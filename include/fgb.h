@@ -305,7 +305,8 @@ size_t fgb_moe_ffn_workspace_bytes(int64_t T, int32_t top_k, int32_t E, int64_t 
  *             contents ignored on entry.
  * 0 <= T <= 64 (more tokens: fgb_grouped_w8a8_block_gemm), T * top_k <= 1024, 1 <= E <= 1024, H and I
  * multiples of 128 up to 32768 (FGB_ERR_SHAPE otherwise).  Only routed experts' weights
- * are read; results do not depend on the order of execution.
+ * are read; results do not depend on the order of execution.  A NaN in a token's row, or in an expert's
+ * codes or scales, is not hidden by the quantizations: it reaches the outputs that it enters, and no other.
  */
 int fgb_moe_ffn(const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int32_t top_k,
                 const uint8_t* w13_q, const void* s_w13, const uint8_t* w2_q, const void* s_w2, int s_w_fmt,
