@@ -3,8 +3,8 @@
 //
 //   score    softmax: p_e = exp(l_e - max l) / sum_j exp(l_j - max l);  sigmoid: p_e = 1 / (1 + exp(-l_e))
 //   select   the k largest of key_e = l_e (both scores grow with l), or of p_e + bias_e with a selection
-//            bias; equal keys go to the lowest index.  A masked expert (l = -inf or NaN) is never
-//            selected: a row with fewer than k open experts fills up with id -1 and weight 0.
+//            bias; equal keys go to the lowest index.  A masked expert (l = -inf or NaN, or a NaN
+//            bias) is never selected: a row with fewer than k open experts fills up with id -1 and weight 0.
 //   weight   p_e, or p_e / (sum of the selected p) renormalized, times a scale.
 //
 // One wave per token, or 16 lanes with many tokens, the row in registers (expert lane + 64 v in register
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * RT_WAVES) void moe_route_kernel(RouteArgs p) {
       const float b = gload<float>(p.bias + min(lane + 64 * v, p.E - 1));
       f = (p.scoring == 0 ? expf(f - row_max) / row_sum : sigmoid_exact(f)) + b + 0.0f;
     }
-    key[v] = l[v] > -inf ? order_key(f) : 0u;
+    key[v] = l[v] > -inf && f == f ? order_key(f) : 0u;  // (a NaN bias; its pattern would order above +inf)
   }
   // lane j keeps the j-th selection
   int my_id = -1;
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs p) {
       const float b = gload<float>(p.bias + min(sub + 16 * v, p.E - 1));
       f = (p.scoring == 0 ? expf(f - row_max) / row_sum : sigmoid_exact(f)) + b + 0.0f;
     }
-    key[v] = l[v] > -inf ? order_key(f) : 0u;
+    key[v] = l[v] > -inf && f == f ? order_key(f) : 0u;  // (a NaN bias; its pattern would order above +inf)
   }
   // lane j of the row keeps the j-th selection
   int my_id = -1;

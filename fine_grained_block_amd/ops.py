@@ -457,8 +457,8 @@ def moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", select
     logits bf16 or float32 [T, E] (unit inner stride).  The top_k largest of each row (ties: the lowest
     index); with `select_bias` float32 [E] the largest of score + select_bias.  Weights are the scores
     ("softmax" over the row or "sigmoid"), divided by the row's selected sum if `renormalize`, times
-    `scale`.  Experts at -inf (or NaN) are never selected: a row without top_k others ends in id -1 and
-    weight 0.  `out` = (ids, weights) writes into given contiguous buffers.
+    `scale`.  Experts at -inf (or NaN, or with a NaN bias) are never selected: a row without top_k others
+    ends in id -1 and weight 0.  `out` = (ids, weights) writes into given contiguous buffers.
     """
     _need(isinstance(logits, torch.Tensor) and logits.dtype in _VALUES, "logits must be bf16 or float32")
     _matrix(logits, "logits", logits.dtype)

@@ -269,7 +269,8 @@ int fgb_check_expert_offsets(const int32_t* expert_offsets, int32_t E, int64_t t
  *   keys     the logits (both scores grow with them), or p + select_bias with a selection bias, which
  *            does not enter the weights; equal keys go to the lowest index.  (With a bias, keys that
  *            differ by less than the float32 rounding of p + select_bias may come in either order.)
- *   masking  an expert whose logit is -inf or NaN is never selected and has no share of the softmax;
+ *   masking  an expert whose logit is -inf or NaN is never selected and has no share of the softmax (+inf
+ *            counts as the largest finite value), one whose select_bias is NaN is never selected;
  *            a row with fewer than top_k open experts ends in ids -1 with weight 0.
  *   weights  p, or with renormalize != 0 p / (sum of the row's selected p), times `scale`.
  *   logits   [T, ld] bf16 or float32 per logits_dtype (fgb_out_dtype values), ld >= E, aligned to the

@@ -48,7 +48,7 @@ def route_ref(logits, top_k: int, scoring: str = "softmax", select_bias=None, re
     """Top-k experts of every row and their weights in float64.
 
     Keys are the logits, or score + select_bias; ties go to the lowest index; experts at -inf (or NaN)
-    are never selected and have no share.  Returns (ids int32 [T, k], weights float64 [T, k], keys
+    are never selected and have no share, experts with a NaN bias are never selected.  Returns (ids int32 [T, k], weights float64 [T, k], keys
     float64 [T, E] with -inf for masked experts)."""
     l = np.asarray(logits, dtype=np.float64)
     l = np.where(np.isnan(l), -np.inf, np.minimum(l, np.finfo(np.float32).max))
@@ -67,6 +67,10 @@ def route_ref(logits, top_k: int, scoring: str = "softmax", select_bias=None, re
         else:  # log sigmoid(v)
             logp = np.minimum(v, 0.0) - np.log1p(np.exp(-np.abs(v)))
         key = v if select_bias is None else np.exp(logp) + np.asarray(select_bias, dtype=np.float64)[open_]
+        there = ~np.isnan(key)
+        if not there.any():
+            continue
+        open_, logp, key = open_[there], logp[there], key[there]
         keys[t, open_] = key
         order = np.lexsort((open_, -key))[:top_k]
         lp = logp[order]
