@@ -60,54 +60,37 @@ __device__ __forceinline__ void activate(int act, float (&v)[W]) {
   });
 }
 
-// W (4 or 8) consecutive values of a bf16 (dtype 0) or float32 (dtype 1) array from element idx,
-// idx a multiple of W, as float32.
-template <int W>
-__device__ __forceinline__ void load_values(const void* p, int dtype, int64_t idx, float (&v)[W]) {
-  static_assert(W == 4 || W == 8, "4 or 8 values");
+// 4 consecutive values of a bf16 (dtype 0) or float32 (dtype 1) array from element idx, a multiple of 4,
+// as float32.
+__device__ __forceinline__ void load_values(const void* p, int dtype, int64_t idx, float (&v)[4]) {
   if (dtype == 0) {
-    uint32_t w[W / 2];
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + idx;
-    if constexpr (W == 8) {
-      const v4i t = gload<v4i>(q);
+    const v2u t = gload<v2u>(reinterpret_cast<const uint16_t*>(p) + idx);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)t[i];
-    } else {
-      const v2u t = gload<v2u>(q);
-      w[0] = t[0];
-      w[1] = t[1];
-    }
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = bf16_lo(t[i]);
+      v[2 * i + 1] = bf16_hi(t[i]);
     }
   } else {
-    const float* q = reinterpret_cast<const float*>(p) + idx;
+    const v4f t = gload<v4f>(reinterpret_cast<const float*>(p) + idx);
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const v4f t = gload<v4f>(q + 4 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * i + j] = t[j];
-    }
+    for (int i = 0; i < 4; ++i) v[i] = t[i];
   }
 }
 
-// W consecutive outputs of row m from column n.
-template <int W>
-__device__ __forceinline__ void epilogue_values(const Epilogue& e, int64_t m, int64_t n, float (&v)[W]) {
+// 4 consecutive outputs of row m from column n.
+__device__ __forceinline__ void epilogue_values(const Epilogue& e, int64_t m, int64_t n, float (&v)[4]) {
   if (e.bias != nullptr) {
-    float b[W];
-    load_values<W>(e.bias, e.bias_dtype, n, b);
+    float b[4];
+    load_values(e.bias, e.bias_dtype, n, b);
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += b[i];
+    for (int i = 0; i < 4; ++i) v[i] += b[i];
   }
-  activate<W>(e.act, v);
+  activate<4>(e.act, v);
   if (e.residual != nullptr) {
-    float r[W];
-    load_values<W>(e.residual, e.residual_dtype, m * e.ldr + n, r);
+    float r[4];
+    load_values(e.residual, e.residual_dtype, m * e.ldr + n, r);
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += r[i];
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
   }
 }
 
@@ -116,7 +99,7 @@ template <int OUT, typename Args>
 __device__ __forceinline__ void store_out(const Args& p, int64_t m, int64_t n, v4f a) {
   if constexpr (Args::kEpilogue) {
     float v[4] = {a[0], a[1], a[2], a[3]};
-    epilogue_values<4>(p.ep, m, n, v);
+    epilogue_values(p.ep, m, n, v);
     a = v4f{v[0], v[1], v[2], v[3]};
   }
   store4<OUT>(p.y, p.ldy, m, n, a);

@@ -315,7 +315,7 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
     if (p.ep.bias != nullptr) {
       for (int c = tid * 4; c < C::BN; c += C::THREADS * 4) {
         float b[4];
-        load_values<4>(p.ep.bias, p.ep.bias_dtype, n0 + c, b);
+        load_values(p.ep.bias, p.ep.bias_dtype, n0 + c, b);
         *reinterpret_cast<v4f*>(bias_lds + c) = v4f{b[0], b[1], b[2], b[3]};
       }
     }
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
 #pragma unroll
       for (int q = 0; q < 8; ++q) bias[q] = bias_lds[ch * 8 + q];
     }
-    const bool res16 = p.ep.residual_dtype == 0, res32 = !res16;
+    const bool res16 = p.ep.residual_dtype == 0;
     const int wrow = wm * (C::BM / C::WM);
 #pragma unroll
     for (int r = 0; r < C::BM / RPR; ++r) {
@@ -584,11 +584,14 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void gemm_prefill_kernel(Args 
               v[2 * q] += bf16_lo((uint32_t)res[it][q]);
               v[2 * q + 1] += bf16_hi((uint32_t)res[it][q]);
             }
-          } else if (res32) {
-            float f[8];
-            load_values<8>(p.ep.residual, 1, m * p.ep.ldr + ncol, f);
+          } else {
+            const float* const f = reinterpret_cast<const float*>(p.ep.residual) + m * p.ep.ldr + ncol;
+            const v4f f0 = gload<v4f>(f), f1 = gload<v4f>(f + 4);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += f[q];
+            for (int q = 0; q < 4; ++q) {
+              v[q] += f0[q];
+              v[4 + q] += f1[q];
+            }
           }
           if constexpr (OUT == 0) {
             v4i w;

@@ -717,7 +717,7 @@ __global__ __launch_bounds__(256) void moe_down_finish_kernel(MoeArgs p, Space s
   for (int z = 0; z < slices; ++z) sum += gload<v4f>(s.yp + ((int64_t)z * p.T + t) * p.H + n);
   if (p.residual != nullptr) {
     float f[4];
-    load_values<4>(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n, f);
+    load_values(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n, f);
     sum += v4f{f[0], f[1], f[2], f[3]};
   }
   store4<OUT>(p.y, p.ldy, t, n, sum);
@@ -902,7 +902,7 @@ __global__ __launch_bounds__(64 * WK) void moe_down_kernel(MoeArgs p, Space s) {
     }
     if (p.residual != nullptr) {
       float f[4];
-      load_values<4>(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n0 + c, f);
+      load_values(p.residual, p.residual_dtype, (int64_t)t * p.ldr + n0 + c, f);
       sum += v4f{f[0], f[1], f[2], f[3]};
     }
     store4<OUT>(p.y, p.ldy, t, n0 + c, sum);
