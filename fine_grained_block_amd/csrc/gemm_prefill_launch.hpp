@@ -58,7 +58,8 @@ hipError_t launch_prefill_kernels(const Args& a, void* workspace, hipStream_t st
     Args b = a;
     b.N = n_big;
     const int tiles_m = (int)((b.M + Big::BM - 1) / Big::BM);
-    // (the epilogue runs in the one-tile-per-workgroup kernel)
+    // (the epilogue runs in the one-tile-per-workgroup kernel: 8192 x 24576 x 1536 with nothing to apply 302 us,
+    // 326 with bias and silu, where the plain GEMM takes 274)
     bool launched = false;
     if constexpr (!Args::kEpilogue) {
       if (use_persistent(b, 16)) {

@@ -12,7 +12,8 @@ fp8        E4M3 / E5M2 / UE8M0 decode and encode from the bit fields (float64, e
 blockquant act_quant (dynamic 1x128 groups), weight_quant (128x128 blocks, float32 or UE8M0)
 gemm       gemm_ref (exact per-block partials, float64), gemm_ref_fast, grouped_ref,
            batched_ref (masked [E, max_M] expert slots), bf16_rne
-feedforward  the GEMM epilogue (bias, activation, residual) in float64
+feedforward  the GEMM epilogue (bias, activation, residual), the router and the mixture-of-experts layer,
+           in float64
 schemes    per-token / per-channel (FP8_DYNAMIC) and static per-tensor quantization, E5M2 codes,
            and the GEMM under those scales (scaled_gemm_ref)
 
