@@ -23,8 +23,8 @@
  *     status words: 4-byte aligned), else FGB_ERR_ALIGN.
  *   - M == 0 (or total_M == 0) is a valid no-op returning FGB_OK.
  *   - N and K must be multiples of 128 (the block edge), else FGB_ERR_SHAPE.
- *   - Inputs must be finite and codes must not be NaN (0x7F/0xFF); otherwise results are
- *     unspecified (no fault, but no meaning either).
+ *   - Unless a call says otherwise, inputs must be finite and codes must not be NaN (0x7F/0xFF);
+ *     otherwise results are unspecified (no fault, but no meaning either).
  */
 #ifndef FGB_H
 #define FGB_H
